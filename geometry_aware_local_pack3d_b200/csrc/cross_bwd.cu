@@ -1,0 +1,769 @@
+// Cross attention, backward, bf16 on tcgen05 tensor cores (head_dim 48, 64, 96 or 128).
+//
+//   p_ij = exp(tau <q_i, k_j> - lse_i),  D_i = <dO_i, o_i>,  dS_ij = p_ij (<dO_i, v_j> - D_i) tau,
+//   dq_i = sum_j dS_ij k_j,   dk_j = sum_i dS_ij q_i,   dv_j = sum_i p_ij dO_i.
+//
+//   k_cross_rows  per row (-lse log2(e), D tau), padded to whole tiles of rows
+//   k_cross_dq    row-major: a CTA walks 128-row tiles; per 64 states S = q K^T and dP = dO V^T,
+//                 dS in bf16 over S, dq += dS K. Two CTAs per SM, so that one tile's products run
+//                 under the other's elementwise pass and epilogue.
+//   k_cross_dkv   state-major: a CTA owns 128 states of one problem and a range of rows; per 64 rows
+//                 S^T = K q^T and dP^T = V dO^T (double-buffered in TMEM), P^T and dS^T in bf16 over
+//                 them, dv += P^T dO and dk += dS^T q. Two groups of elementwise warps take turns.
+//   k_cross_sum   the row ranges' partial dk, dv, added in range order (no atomics anywhere).
+// A KV head's gradients sum over its query heads, which are rows of the same problem.
+// P and dS are rounded to bf16 for the second products (relative 2^-9, as the outputs).
+// Masked states: in k_cross_dq their dS is zero whatever S and dP hold, and their K rows (which may
+// hold NaN) are zeroed in shared memory; in k_cross_dkv each state is an output row of its own, so
+// the masked rows' sums are simply not written and zeros are.
+#include <math.h>
+
+#include "cross_tc.cuh"
+#include "launch.h"
+
+namespace p3d {
+namespace xa {
+
+namespace xb {
+constexpr int kHalf = 64;  // states per step (dq), rows per step (dkv)
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 f2(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+
+struct Params {
+  const float2* rows;  // [bh][npad]
+  const int32_t* act;
+  const uint4* bits;
+  int32_t* status;
+  long long budget;
+  int64_t np, npad, l, bh, units;
+  int rtiles, tiles, kv_heads, nsplit;
+  float scale, scale_log2;
+  __nv_bfloat16 *dk, *dv;   // written when nsplit is 1
+  float *part_k, *part_v;   // [nsplit][bh][l][D] otherwise
+};
+}  // namespace xb
+
+// ------------------------------------------------------------------------------- row data
+template <int D>
+__global__ void __launch_bounds__(256)
+    k_cross_rows(const __nv_bfloat16* __restrict__ dO, const __nv_bfloat16* __restrict__ o,
+                 const float* __restrict__ lse, int64_t np, int64_t npad, int64_t bh, float scale,
+                 float2* __restrict__ rows) {
+  constexpr int G = D <= 64 ? 8 : 16;  // threads per row, a 16-byte piece each
+  const int64_t i = blockIdx.x * (int64_t)(256 / G) + threadIdx.x / G;
+  const int t = threadIdx.x % G;
+  if (i >= bh * npad) return;  // whole groups: the shuffles below stay inside one
+  const int64_t p = i / npad, r = i % npad;
+  const int64_t row = p * np + r;
+  float s = 0.f;
+  if (r < np && t < D / 8) {
+    float a[8], b[8];
+    Vec<__nv_bfloat16>::load(dO + row * D + t * 8, a);
+    Vec<__nv_bfloat16>::load(o + row * D + t * 8, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+  }
+  const uint32_t grp = (G == 16 ? 0xffffu : 0xffu) << (threadIdx.x & 31 & ~(G - 1));
+#pragma unroll
+  for (int x = G / 2; x > 0; x >>= 1) s += __shfl_xor_sync(grp, s, x);
+  if (t == 0) {
+    const float le = r < np ? lse[row] : -INFINITY;
+    // a row without any state, and the padding: P = 0
+    rows[i] = make_float2(le == -INFINITY ? -INFINITY : -le * kLog2e, s * scale);
+  }
+}
+
+// -------------------------------------------------------------------------------------- dq
+namespace xq {
+constexpr int kThreads = 256;  // elementwise 0-3, TMA 4, MMA 5, masked rows of K 6
+template <int D> struct Smem {
+  static constexpr int TB = Lay<D>::bytes(kTile), HB = Lay<D>::bytes(xb::kHalf);
+  static constexpr int kQ = 0, kG = TB, kRing = 2 * TB;
+  // two CTAs per SM: 2 (bytes + 1 KB) within 228 KB
+  static constexpr int kFit = (116736 - 1024 - 512 - kRing) / HB;
+  // V and K take turns (V first: its slot is free before K's, which the step's last product reads)
+  static constexpr int kSlots = kFit < 6 ? kFit : 6;
+  static constexpr int kBar = kRing + kSlots * HB;
+  static constexpr int kBytes = kBar + 512;
+};
+constexpr int kMaxSlots = 6, kReady = 8;
+enum {
+  B_QFULL = 0, B_QEMPTY = 1, B_FULL = 2, B_EMPTY = B_FULL + kMaxSlots,
+  B_READY = B_EMPTY + kMaxSlots, B_SFULL = B_READY + kReady, B_PFULL, B_DONE, B_STAGED, B_DRAIN,
+  B_COUNT
+};
+static_assert(8 * B_COUNT + 16 <= 512, "barrier area");
+constexpr uint32_t kS = 0, kP = 64, kO = 128;  // TMEM columns: S (then dS), dP, dq
+
+// A unit's problem, first row and steps of 64 states (the batch entry's listed tiles, halved).
+struct Unit {
+  int64_t bh, row0;
+  int n;
+  const int32_t* list;
+  const uint4* bits;
+  __device__ __forceinline__ Unit(const xb::Params& P, int64_t u) {
+    bh = u / P.rtiles;
+    row0 = (u % P.rtiles) * kTile;
+    const int64_t b = bh / P.kv_heads;
+    list = nullptr;
+    bits = nullptr;
+    n = (int)((P.l + xb::kHalf - 1) / xb::kHalf);
+    if (P.act) {
+      list = P.act + b * (P.tiles + 1) + 1;
+      bits = P.bits + b * P.tiles;
+      n = 2 * list[-1];
+    }
+  }
+  __device__ __forceinline__ int64_t at(int j) const {
+    return list ? (int64_t)list[j >> 1] * kTile + (j & 1) * xb::kHalf : (int64_t)j * xb::kHalf;
+  }
+  __device__ __forceinline__ void words(int64_t l, int j, uint32_t (&w)[2]) const {
+    if (bits) {
+      const uint2 b = reinterpret_cast<const uint2*>(bits)[2 * list[j >> 1] + (j & 1)];
+      w[0] = b.x;
+      w[1] = b.y;
+    } else {
+      const int64_t left = l - (int64_t)j * xb::kHalf;
+      w[0] = left >= 32 ? ~0u : (1u << left) - 1u;
+      w[1] = left >= 64 ? ~0u : (left <= 32 ? 0u : (1u << (left - 32)) - 1u);
+    }
+  }
+};
+}  // namespace xq
+
+template <int D>
+__global__ void __launch_bounds__(xq::kThreads, 2)
+    k_cross_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
+               const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+               const __grid_constant__ CUtensorMap mo, const xb::Params P) {
+  using namespace xq;
+  using S = Smem<D>;
+  using Ly = Lay<D>;
+  constexpr int NS = S::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kBar + 8 * B_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kBar + 8 * B_COUNT + 8);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  tc::Abort ab{abort_flag, P.status, P.budget};
+  if (tid == 0) {
+    tc::mbar_init(&bars[B_QFULL], 1);
+    tc::mbar_init(&bars[B_QEMPTY], 1);
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(&bars[B_FULL + i], 1);
+      tc::mbar_init(&bars[B_EMPTY + i], 1);
+    }
+    for (int i = 0; i < kReady; ++i) tc::mbar_init(&bars[B_READY + i], 1);
+    tc::mbar_init(&bars[B_SFULL], 1);
+    tc::mbar_init(&bars[B_PFULL], 128);
+    tc::mbar_init(&bars[B_DONE], 1);
+    tc::mbar_init(&bars[B_STAGED], 128);
+    tc::mbar_init(&bars[B_DRAIN], 1);
+    abort_flag[0] = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 5) tc::tmem_alloc(tmem_slot, 256);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ elementwise and epilogue
+    const int rin = warp * 32 + lane;
+    const uint32_t tl = tbase + ((uint32_t)(warp * 32) << 16);
+    uint32_t gc = 0, staged = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
+      const Unit U(P, u);
+      const float2 rd = P.rows[U.bh * P.npad + U.row0 + rin];
+      const float2 nl2 = make_float2(rd.x, rd.x), nd2 = make_float2(-rd.y, -rd.y);
+      const float2 sl2 = make_float2(P.scale_log2, P.scale_log2);
+      const float2 sc2 = make_float2(P.scale, P.scale);
+      for (int j = 0; j < U.n; ++j, ++gc) {
+        uint32_t w[2];
+        U.words(P.l, j, w);
+        if (!__all_sync(0xffffffffu, ab.wait(&bars[B_SFULL], gc & 1))) { ok = false; break; }
+        tc::tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t sv[32], dv[32], pk[16];
+          tc::tmem_ld32(tl + kS + 32 * h, sv);
+          tc::tmem_ld32(tl + kP + 32 * h, dv);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 x = tc::fma2(xb::f2(sv[k], sv[k + 1]), sl2, nl2);
+            const float2 t = tc::fma2(xb::f2(dv[k], dv[k + 1]), sc2, nd2);
+            float2 ds = xb::mul2(make_float2(ex2(x.x), ex2(x.y)), t);
+            if (w[h] != 0xffffffffu) {
+              ds.x = ((w[h] >> k) & 1u) ? ds.x : 0.f;
+              ds.y = ((w[h] >> (k + 1)) & 1u) ? ds.y : 0.f;
+            }
+            pk[k >> 1] = tc::pack_bf16(ds.x, ds.y);
+          }
+          // over S columns that this thread has read
+          tc::tmem_st16(tl + kS + 16 * h, pk);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::mbar_arrive(&bars[B_PFULL]);
+      }
+      if (!ok) break;
+      if (U.n && !__all_sync(0xffffffffu, ab.wait(&bars[B_DONE], (gc - 1) & 1))) break;
+      if (!U.n) {
+        // no state: zero rows
+        if (U.row0 + rin < P.np) {
+          __nv_bfloat16* dst = P.dk + (U.bh * P.np + U.row0 + rin) * D;
+#pragma unroll
+          for (int e = 0; e < D; e += 8)
+            *reinterpret_cast<uint4*>(dst + e) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      tc::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        tc::tmem_ld16(tl + kO + c, o);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            pk[i] = tc::pack_bf16(__uint_as_float(o[8 * h + 2 * i]),
+                                  __uint_as_float(o[8 * h + 2 * i + 1]));
+          // the q tile has been consumed: its buffer takes the gradient's rows
+          *reinterpret_cast<uint4*>(smem + S::kQ + Ly::piece(kTile, rin, c / 8 + h)) =
+              make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+      }
+      tc::tc_fence_before();
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive(&bars[B_STAGED]);
+      if (rin == 0) {
+        if (!ab.wait(&bars[B_STAGED], staged++ & 1)) ok = false;
+#pragma unroll
+        for (int c = 0; c < Ly::NB && ok; ++c)
+          tma_store_3d(&mo, smem + S::kQ + c * kTile * Ly::RB, c * Ly::CW, (int)U.row0, (int)U.bh);
+        bulk_commit();
+        bulk_wait_read();
+        tc::mbar_arrive(&bars[B_QEMPTY]);
+      }
+      ok = __all_sync(0xffffffffu, ok);  // a warp leaves the loop as one
+    }
+    if (rin == 0) bulk_wait();
+  } else if (warp == 4) {
+    // ------------------------------------------------------------ TMA loads
+    if (lane == 0) {
+      uint32_t kv = 0, uc = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
+        const Unit U(P, u);
+        if (!U.n) continue;
+        if (uc && !ab.wait(&bars[B_QEMPTY], (uc - 1) & 1)) break;
+        tc::mbar_expect_tx(&bars[B_QFULL], 2 * S::TB);
+        load_rows<D>(smem + S::kQ, &mq, kTile, U.row0, (int)U.bh, &bars[B_QFULL]);
+        load_rows<D>(smem + S::kG, &mg, kTile, U.row0, (int)U.bh, &bars[B_QFULL]);
+        ++uc;
+        for (int j = 0; j < U.n && ok; ++j) {
+          const int64_t at = U.at(j);
+          for (int x = 0; x < 2; ++x, ++kv) {
+            const int st = kv % NS;
+            if (kv >= (uint32_t)NS && !ab.wait(&bars[B_EMPTY + st], ((kv / NS) - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc::mbar_expect_tx(&bars[B_FULL + st], S::HB);
+            load_rows<D>(smem + S::kRing + st * S::HB, x ? &mk : &mv, xb::kHalf, at, (int)U.bh,
+                         &bars[B_FULL + st]);
+          }
+        }
+      }
+      for (uint32_t k = kv > (uint32_t)NS ? kv - NS : 0; k < kv; ++k)
+        tc::mbar_wait(&bars[B_FULL + (k % NS)], (k / NS) & 1);
+      if (uc) tc::mbar_wait(&bars[B_QFULL], (uc - 1) & 1);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+    const uint32_t id_s = tc::idesc_bf16_f32(128, xb::kHalf, false, false);
+    const uint32_t id_o = tc::idesc_bf16_f32(128, D, false, true);
+    const uint64_t qd = Ly::kdesc(tc::smem_u32(smem + S::kQ));
+    const uint64_t gd = Ly::kdesc(tc::smem_u32(smem + S::kG));
+    const uint64_t kd0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
+    const uint64_t km0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
+    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, ab.wait(bar, parity, false));
+    };
+    const bool masked = P.act != nullptr;
+    uint32_t kv = 0, gc = 0, uc = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
+      const Unit U(P, u);
+      if (!U.n) continue;
+      if (!wwait(&bars[B_QFULL], uc & 1)) break;
+      ++uc;
+      for (int j = 0; j < U.n; ++j, ++gc, kv += 2) {
+        const int sv = kv % NS, sk = (kv + 1) % NS;
+        ok = masked ? wwait(&bars[B_READY + gc % kReady], (gc / kReady) & 1)
+                    : wwait(&bars[B_FULL + sk], ((kv + 1) / NS) & 1);
+        ok = ok && wwait(&bars[B_FULL + sv], (kv / NS) & 1);
+        // S and dP hold the previous step's dS until its product has completed
+        if (ok && gc >= 1) ok = wwait(&bars[B_DONE], (gc - 1) & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t ko = (uint64_t)((sk * S::HB) >> 4), vo = (uint64_t)((sv * S::HB) >> 4);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < Ly::kSteps; ++ks) {
+            tc::mma_ss(tb + kS, qd + Ly::koff(kTile, ks), kd0 + ko + Ly::koff(xb::kHalf, ks), id_s,
+                       ks > 0);
+            tc::mma_ss(tb + kP, gd + Ly::koff(kTile, ks), kd0 + vo + Ly::koff(xb::kHalf, ks), id_s,
+                       ks > 0);
+          }
+          tc::tc_commit(&bars[B_SFULL]);
+          tc::tc_commit(&bars[B_EMPTY + sv]);
+        }
+        __syncwarp();
+        if (!wwait(&bars[B_PFULL], gc & 1)) { ok = false; break; }
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < xb::kHalf / 16; ++ks)
+            tc::mma_ts(tb + kO, tb + kS + ks * 8, km0 + ko + Ly::moff(ks), id_o,
+                       (j > 0 || ks > 0) ? 1u : 0u);
+          tc::tc_commit(&bars[B_DONE]);
+          tc::tc_commit(&bars[B_EMPTY + sk]);
+        }
+        __syncwarp();
+      }
+    }
+    if (tc::elect_one()) tc::tc_commit(&bars[B_DRAIN]);
+    __syncwarp();
+    if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) set_status(P.status, PACK3D_ERR_TIMEOUT);
+  } else if (warp == 6 && P.act) {
+    // ------------------------------------------------------------ masked rows of K
+    uint32_t g = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
+      const Unit U(P, u);
+      for (int j = 0; j < U.n; ++j, ++g) {
+        uint32_t w[2];
+        U.words(P.l, j, w);
+        const uint32_t kv = 2 * g + 1;
+        const int st = kv % NS;
+        ok = __all_sync(0xffffffffu, ab.wait(&bars[B_FULL + st], (kv / NS) & 1));
+        if (!ok) break;
+        if ((w[0] & w[1]) != 0xffffffffu) {
+          uint8_t* kt = smem + S::kRing + st * S::HB;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!((w[i] >> lane) & 1u))
+#pragma unroll
+              for (int pc = 0; pc < D / 8; ++pc)
+                *reinterpret_cast<uint4*>(kt + Ly::piece(xb::kHalf, 32 * i + lane, pc)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          tc::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars[B_READY + g % kReady]);
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tbase, 256);
+  }
+}
+
+// ---------------------------------------------------------------------------------- dk, dv
+namespace xk {
+constexpr int kThreads = 320;  // elementwise 0-3 (even steps), 4-7 (odd), TMA 8, MMA 9
+template <int D> struct Smem {
+  static constexpr int TB = Lay<D>::bytes(kTile), HB = Lay<D>::bytes(xb::kHalf);
+  static constexpr int kK = 0, kV = TB, kRing = 2 * TB;
+  static constexpr int kRowB = xb::kHalf * 8;               // (-lse log2(e), D tau) of a step's rows
+  static constexpr int kStages = 4;
+  static constexpr int kRows = kRing + kStages * 2 * HB;    // [stages]
+  static constexpr int kBar = kRows + kStages * kRowB;
+  static constexpr int kBytes = kBar + 512;
+};
+constexpr int kStages = 4;
+enum {
+  B_AFULL = 0, B_QFULL = 1, B_QEMPTY = B_QFULL + kStages, B_SFULL = B_QEMPTY + kStages,
+  B_PFULL = B_SFULL + 2, B_DONE = B_PFULL + 2, B_ALL = B_DONE + 2, B_DRAIN, B_COUNT
+};
+static_assert(8 * B_COUNT + 16 <= 512, "barrier area");
+// TMEM columns: dk, dv; S^T and dP^T of step i in buffer i % 2
+constexpr uint32_t kK = 0, kV = 128;
+__device__ __forceinline__ uint32_t s_col(int b) { return 256u + 128u * b; }
+__device__ __forceinline__ uint32_t p_col(int b) { return 320u + 128u * b; }
+}  // namespace xk
+
+template <int D>
+__global__ void __launch_bounds__(xk::kThreads, 1)
+    k_cross_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
+                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                const xb::Params P) {
+  using namespace xk;
+  using S = Smem<D>;
+  using Ly = Lay<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kBar + 8 * B_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kBar + 8 * B_COUNT + 8);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  tc::Abort ab{abort_flag, P.status, P.budget};
+  const int64_t item = blockIdx.x;
+  const int split = (int)(item % P.nsplit);
+  const int kt = (int)((item / P.nsplit) % P.tiles);
+  const int64_t bh = item / ((int64_t)P.nsplit * P.tiles);
+  uint32_t w[4];
+  if (P.act) {
+    const uint4 b = P.bits[bh / P.kv_heads * P.tiles + kt];
+    w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
+  } else {
+    tail_words(P.l, kt, w);
+  }
+  const bool any = (w[0] | w[1] | w[2] | w[3]) != 0u;
+  const int64_t steps = (P.np + xb::kHalf - 1) / xb::kHalf;
+  const int64_t i0 = steps * split / P.nsplit;
+  const int NT = any ? (int)(steps * (split + 1) / P.nsplit - i0) : 0;
+  if (tid == 0) {
+    tc::mbar_init(&bars[B_AFULL], 1);
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&bars[B_QFULL + i], 1);
+      tc::mbar_init(&bars[B_QEMPTY + i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bars[B_SFULL + i], 1);
+      tc::mbar_init(&bars[B_PFULL + i], 128);
+      tc::mbar_init(&bars[B_DONE + i], 1);
+    }
+    tc::mbar_init(&bars[B_ALL], 1);
+    tc::mbar_init(&bars[B_DRAIN], 1);
+    abort_flag[0] = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 9) tc::tmem_alloc(tmem_slot, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ elementwise and epilogue
+    const int b = warp >> 2, rin = (warp & 3) * 32 + lane;
+    const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+    const float2 sl2 = make_float2(P.scale_log2, P.scale_log2);
+    const float2 sc2 = make_float2(P.scale, P.scale);
+    bool ok = true;
+    for (int i = b; i < NT; i += 2) {
+      if (!__all_sync(0xffffffffu, ab.wait(&bars[B_SFULL + b], (i >> 1) & 1))) { ok = false; break; }
+      // the row data came with the step's tiles
+      if (!__all_sync(0xffffffffu, ab.wait(&bars[B_QFULL + i % kStages], (i / kStages) & 1))) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      // one 16-byte read brings two rows' data (every thread reads the same)
+      const float4* rd =
+          reinterpret_cast<const float4*>(smem + S::kRows + (i % kStages) * S::kRowB);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t sv[32], dv[32], pp[16], pd[16];
+        tc::tmem_ld32(tl + s_col(b) + 32 * h, sv);
+        tc::tmem_ld32(tl + p_col(b) + 32 * h, dv);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float4 r = rd[16 * h + (k >> 1)];
+          const float2 x = tc::fma2(xb::f2(sv[k], sv[k + 1]), sl2, make_float2(r.x, r.z));
+          const float2 p = make_float2(ex2(x.x), ex2(x.y));
+          const float2 t = tc::fma2(xb::f2(dv[k], dv[k + 1]), sc2, make_float2(-r.y, -r.w));
+          const float2 ds = xb::mul2(p, t);
+          pp[k >> 1] = tc::pack_bf16(p.x, p.y);
+          pd[k >> 1] = tc::pack_bf16(ds.x, ds.y);
+        }
+        tc::tmem_st16(tl + s_col(b) + 16 * h, pp);
+        tc::tmem_st16(tl + p_col(b) + 16 * h, pd);
+      }
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      tc::mbar_arrive(&bars[B_PFULL + b]);
+    }
+    // warps 0-3 write dk, warps 4-7 dv, once every step's products have completed (a barrier of
+    // its own: a group has not followed the other group's phases of B_DONE)
+    const int64_t row = (int64_t)kt * kTile + rin;
+    const bool in = (w[rin >> 5] >> (rin & 31)) & 1u;
+    if (ok && NT > 0) ok = __all_sync(0xffffffffu, ab.wait(&bars[B_ALL], 0));
+    tc::tc_fence_after();
+    if (ok) {
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        uint32_t a[16];
+        if (NT > 0) {
+          tc::tmem_ld16(tl + (b ? kV : kK) + c, a);
+          tc::tmem_wait_ld();
+        }
+        if (NT == 0 || !in)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) a[e] = 0u;
+        if (row < P.l) {
+          if (P.nsplit > 1) {
+            float* dst = (b ? P.part_v : P.part_k) + ((split * P.bh + bh) * P.l + row) * D + c;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<uint4*>(dst + e) = make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]);
+          } else {
+            __nv_bfloat16* dst = (b ? P.dv : P.dk) + (bh * P.l + row) * D + c;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                pk[e] = tc::pack_bf16(__uint_as_float(a[8 * h + 2 * e]),
+                                      __uint_as_float(a[8 * h + 2 * e + 1]));
+              *reinterpret_cast<uint4*>(dst + 8 * h) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          }
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0 && NT > 0) {
+      tc::mbar_expect_tx(&bars[B_AFULL], 2 * S::TB);
+      load_rows<D>(smem + S::kK, &mk, kTile, (int64_t)kt * kTile, (int)bh, &bars[B_AFULL]);
+      load_rows<D>(smem + S::kV, &mv, kTile, (int64_t)kt * kTile, (int)bh, &bars[B_AFULL]);
+      int i = 0;
+      for (; i < NT; ++i) {
+        const int st = i % kStages;
+        if (i >= kStages && !ab.wait(&bars[B_QEMPTY + st], ((i / kStages) - 1) & 1)) break;
+        const int64_t row = (i0 + i) * xb::kHalf;
+        tc::mbar_expect_tx(&bars[B_QFULL + st], 2 * S::HB + S::kRowB);
+        load_rows<D>(smem + S::kRing + 2 * st * S::HB, &mq, xb::kHalf, row, (int)bh,
+                     &bars[B_QFULL + st]);
+        load_rows<D>(smem + S::kRing + (2 * st + 1) * S::HB, &mg, xb::kHalf, row, (int)bh,
+                     &bars[B_QFULL + st]);
+        tc::bulk_g2s(smem + S::kRows + st * S::kRowB, P.rows + bh * P.npad + row, S::kRowB,
+                     &bars[B_QFULL + st]);
+      }
+      tc::mbar_wait(&bars[B_AFULL], 0);
+      for (int k = i > kStages ? i - kStages : 0; k < i; ++k)
+        tc::mbar_wait(&bars[B_QFULL + (k % kStages)], (k / kStages) & 1);
+    }
+  } else {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+    const uint32_t id_s = tc::idesc_bf16_f32(128, xb::kHalf, false, false);
+    const uint32_t id_o = tc::idesc_bf16_f32(128, D, false, true);
+    const uint64_t kd = Ly::kdesc(tc::smem_u32(smem + S::kK));
+    const uint64_t vd = Ly::kdesc(tc::smem_u32(smem + S::kV));
+    const uint64_t rk0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
+    const uint64_t rm0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
+    constexpr uint64_t HO = (uint64_t)(S::HB >> 4);
+    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, ab.wait(bar, parity, false));
+    };
+    // S^T and dP^T of step i into buffer i % 2, free once step i - 2's products completed
+    auto issue_s = [&](int i) -> bool {
+      const int st = i % kStages, b = i & 1;
+      if (!wwait(&bars[B_QFULL + st], (i / kStages) & 1)) return false;
+      if (i >= 2 && !wwait(&bars[B_DONE + b], ((i - 2) >> 1) & 1)) return false;
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+        const uint64_t qo = rk0 + 2 * st * HO, go = qo + HO;
+#pragma unroll
+        for (int ks = 0; ks < Ly::kSteps; ++ks) {
+          tc::mma_ss(tb + s_col(b), kd + Ly::koff(kTile, ks), qo + Ly::koff(xb::kHalf, ks), id_s,
+                     ks > 0);
+          tc::mma_ss(tb + p_col(b), vd + Ly::koff(kTile, ks), go + Ly::koff(xb::kHalf, ks), id_s,
+                     ks > 0);
+        }
+        tc::tc_commit(&bars[B_SFULL + b]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = NT > 0 && wwait(&bars[B_AFULL], 0);
+    for (int i = 0; i < 2 && i < NT && ok; ++i) ok = issue_s(i);
+    for (int i = 0; i < NT && ok; ++i) {
+      const int st = i % kStages, b = i & 1;
+      if (!wwait(&bars[B_PFULL + b], (i >> 1) & 1)) break;
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+        const uint64_t qm = rm0 + 2 * st * HO, gm = qm + HO;
+#pragma unroll
+        for (int ks = 0; ks < xb::kHalf / 16; ++ks) {
+          tc::mma_ts(tb + kV, tb + s_col(b) + ks * 8, gm + Ly::moff(ks), id_o,
+                     (i > 0 || ks > 0) ? 1u : 0u);
+          tc::mma_ts(tb + kK, tb + p_col(b) + ks * 8, qm + Ly::moff(ks), id_o,
+                     (i > 0 || ks > 0) ? 1u : 0u);
+        }
+        tc::tc_commit(&bars[B_QEMPTY + st]);
+        tc::tc_commit(&bars[B_DONE + b]);
+        if (i == NT - 1) tc::tc_commit(&bars[B_ALL]);
+      }
+      __syncwarp();
+      if (i + 2 < NT) ok = issue_s(i + 2);
+    }
+    if (tc::elect_one()) tc::tc_commit(&bars[B_DRAIN]);
+    __syncwarp();
+    if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) set_status(P.status, PACK3D_ERR_TIMEOUT);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tbase, 512);
+  }
+}
+
+// dk, dv = sum over the row ranges, in order: four elements per thread
+__global__ void __launch_bounds__(256)
+    k_cross_sum(const float* __restrict__ pk, const float* __restrict__ pv, int nsplit, int64_t n,
+                __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+  const int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 4;
+  if (i >= n) return;
+  const float* p = (blockIdx.y ? pv : pk) + i;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < nsplit; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(p + k * n);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  *reinterpret_cast<uint2*>((blockIdx.y ? dv : dk) + i) =
+      make_uint2(tc::pack_bf16(s.x, s.y), tc::pack_bf16(s.z, s.w));
+}
+
+// Row ranges of the state-major kernel (one CTA per SM): the count whose CTAs fill the last wave
+// best, the fewest on a tie, with at least four steps of 64 rows in a range.
+static int dkv_ranges(const Problem& p) {
+  const int64_t items = p.bh * p.tiles(), sms = sm_count();
+  const int64_t steps = (p.np + xb::kHalf - 1) / xb::kHalf;
+  const int64_t most = (8 * sms + items - 1) / items;
+  int best = 1;
+  double eff = 0.0;
+  for (int64_t n = 1; n <= most && (n == 1 || n * 4 <= steps); ++n) {
+    const int64_t waves = (items * n + sms - 1) / sms;
+    // a range's fixed cost (loads, epilogue) is about two steps
+    const double per = (double)((steps + n - 1) / n) + 2.0;
+    const double e = (double)steps * items / (waves * sms * per);
+    if (e > eff * 1.001) {
+      eff = e;
+      best = (int)n;
+    }
+  }
+  return best;
+}
+
+size_t bwd_tc_bytes(const Problem& p) {
+  const int64_t npad = (p.np + kTile - 1) / kTile * kTile;
+  const int n = dkv_ranges(p);
+  const size_t e = (size_t)n * p.bh * p.l * p.d * sizeof(float);
+  return align256((size_t)p.bh * npad * sizeof(float2)) + (n > 1 ? 2 * align256(e) : 0);
+}
+
+template <int D>
+static cudaError_t launch_bwd(const Problem& p, const MaskTables& m, const void* o,
+                              const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                              void* ws) {
+  using Sq = xq::Smem<D>;
+  using Sk = xk::Smem<D>;
+  static std::atomic<uint64_t> aq{0}, ak{0};
+  cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(k_cross_dq<D>), Sq::kBytes, aq);
+  if (e == cudaSuccess)
+    e = smem_attr_once(reinterpret_cast<const void*>(k_cross_dkv<D>), Sk::kBytes, ak);
+  if (e != cudaSuccess) return e;
+  CUtensorMap q128, g128, k64, v64, o128, q64, g64, k128, v128;
+  if (!encode_rows<D>(&q128, p.q, p.np, p.bh, kTile) ||
+      !encode_rows<D>(&g128, dO, p.np, p.bh, kTile) ||
+      !encode_rows<D>(&o128, dq, p.np, p.bh, kTile) ||
+      !encode_rows<D>(&k64, p.k, p.l, p.bh, xb::kHalf) ||
+      !encode_rows<D>(&v64, p.v, p.l, p.bh, xb::kHalf) ||
+      !encode_rows<D>(&q64, p.q, p.np, p.bh, xb::kHalf) ||
+      !encode_rows<D>(&g64, dO, p.np, p.bh, xb::kHalf) ||
+      !encode_rows<D>(&k128, p.k, p.l, p.bh, kTile) ||
+      !encode_rows<D>(&v128, p.v, p.l, p.bh, kTile))
+    return cudaErrorInvalidValue;
+  const int64_t npad = (p.np + kTile - 1) / kTile * kTile;
+  float2* rows = static_cast<float2*>(ws);
+  constexpr int per = 256 / (D <= 64 ? 8 : 16);
+  k_cross_rows<D><<<(unsigned)((p.bh * npad + per - 1) / per), 256, 0, p.s>>>(
+      static_cast<const __nv_bfloat16*>(dO), static_cast<const __nv_bfloat16*>(o), lse, p.np, npad,
+      p.bh, p.scale, rows);
+  xb::Params P{};
+  P.rows = rows;
+  P.act = m.act;
+  P.bits = m.bits;
+  P.status = p.status;
+  P.budget = wait_budget_cycles();
+  P.np = p.np;
+  P.npad = npad;
+  P.l = p.l;
+  P.bh = p.bh;
+  P.rtiles = (int)(npad / kTile);
+  P.tiles = (int)p.tiles();
+  P.kv_heads = p.kv_heads;
+  P.scale = p.scale;
+  P.scale_log2 = p.scale * kLog2e;
+  // dq: persistent, two CTAs per SM
+  P.nsplit = 1;
+  P.units = p.bh * P.rtiles;
+  P.dk = static_cast<__nv_bfloat16*>(dq);
+  const int64_t cap = 2 * (int64_t)sm_count();
+  k_cross_dq<D><<<(unsigned)(P.units < cap ? P.units : cap), xq::kThreads, Sq::kBytes, p.s>>>(
+      q128, g128, k64, v64, o128, P);
+  // dk, dv
+  P.nsplit = dkv_ranges(p);
+  P.dk = static_cast<__nv_bfloat16*>(dk);
+  P.dv = static_cast<__nv_bfloat16*>(dv);
+  if (P.nsplit > 1) {
+    uint8_t* at = static_cast<uint8_t*>(ws) + align256((size_t)p.bh * npad * sizeof(float2));
+    P.part_k = reinterpret_cast<float*>(at);
+    P.part_v = reinterpret_cast<float*>(
+        at + align256((size_t)P.nsplit * p.bh * p.l * D * sizeof(float)));
+  }
+  const int64_t items = p.bh * P.tiles * P.nsplit;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  k_cross_dkv<D><<<(unsigned)items, xk::kThreads, Sk::kBytes, p.s>>>(q64, g64, k128, v128, P);
+  count_launch(3);
+  if (P.nsplit > 1) {
+    const int64_t n = p.bh * p.l * D;
+    k_cross_sum<<<dim3((unsigned)((n / 4 + 255) / 256), 2), 256, 0, p.s>>>(
+        P.part_k, P.part_v, P.nsplit, n, P.dk, P.dv);
+    count_launch();
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t bwd_tc(const Problem& p, const MaskTables& m, const void* o, const float* lse,
+                   const void* dO, void* dq, void* dk, void* dv, void* ws) {
+  switch (p.d) {
+    case 48: return launch_bwd<48>(p, m, o, lse, dO, dq, dk, dv, ws);
+    case 64: return launch_bwd<64>(p, m, o, lse, dO, dq, dk, dv, ws);
+    case 96: return launch_bwd<96>(p, m, o, lse, dO, dq, dk, dv, ws);
+    default: return launch_bwd<128>(p, m, o, lse, dO, dq, dk, dv, ws);
+  }
+}
+
+}  // namespace xa
+}  // namespace p3d

@@ -1,0 +1,506 @@
+// Cross attention in fp32 on CUDA cores (no TF32: the 32-bit path keeps 32-bit products), forward
+// and backward, head_dim 48, 64, 96 or 128.
+//
+// Tiles of 64 rows x 64 states; 256 threads as 16 x 16, thread (ty, tx) holding rows 4 ty .. + 3
+// and states tx + 16 j of a score tile. What bounds it: the FMA pipe; a thread's 4 x 4 scores take
+// 64 FMAs per 8 shared loads of 16 bytes. The rows of a masked state are read as zeros, so that
+// nothing they hold reaches a product, and their scores are -inf.
+//   k_cross_fwd32   online softmax over the state tiles, o and lse
+//   k_cross_dq32    dq_i = sum_j dS_ij k_j,            dS = p (dO v - D) tau
+//   k_cross_dkv32   dk_j = sum_i dS_ij q_i,  dv_j = sum_i p_ij dO_i over a range of row tiles; the
+//                   ranges' sums are added in order by k_cross_sum
+// Every sum runs in a fixed order (no atomics).
+#include <math.h>
+
+#include "cross.h"
+#include "launch.h"
+
+namespace p3d {
+namespace xa {
+
+namespace xs {
+constexpr int kT = 64;          // rows, states per tile
+constexpr int kThreads = 256;
+constexpr int kP = kT + 4;      // pitch of a score tile
+template <int D> constexpr int pitch() { return D + 4; }
+
+template <int D>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t row0, int64_t rows,
+                                          uint32_t w0, uint32_t w1) {
+  constexpr int C = D / 4;
+  for (int i = threadIdx.x; i < kT * C; i += kThreads) {
+    const int r = i / C, c = (i % C) * 4;
+    const bool on = row0 + r < rows && (((r < 32 ? w0 : w1) >> (r & 31)) & 1u);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) x = *reinterpret_cast<const float4*>(src + (row0 + r) * D + c);
+    *reinterpret_cast<float4*>(dst + r * pitch<D>() + c) = x;
+  }
+}
+
+// s[i][j] = <a row 4 ty + i, b row tx + 16 j>
+template <int D>
+__device__ __forceinline__ void product(const float* a, const float* b, int ty, int tx,
+                                        float (&s)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < D; c += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = *reinterpret_cast<const float4*>(a + (4 * ty + i) * pitch<D>() + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * pitch<D>() + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+        s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+        s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+        s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+      }
+  }
+}
+
+// acc[i][c] += sum over the 64 inner rows of m[4 ty + i][inner] b[inner][tx + 16 c]
+template <int D>
+__device__ __forceinline__ void accumulate(const float* m, const float* b, int ty, int tx,
+                                           float (&acc)[4][D / 16]) {
+#pragma unroll 2
+  for (int k = 0; k < kT; k += 4) {
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(m + (4 * ty + i) * kP + k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const float y = b[(k + e) * pitch<D>() + tx + 16 * c];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[i][c] = fmaf(e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w, y,
+                           acc[i][c]);
+      }
+    }
+  }
+}
+
+// As accumulate with m transposed: acc[i][c] += sum over rows r of m[r][4 ty + i] b[r][tx + 16 c]
+template <int D>
+__device__ __forceinline__ void accumulate_t(const float* m, const float* b, int ty, int tx,
+                                             float (&acc)[4][D / 16]) {
+#pragma unroll 4
+  for (int r = 0; r < kT; ++r) {
+    const float4 x = *reinterpret_cast<const float4*>(m + r * kP + 4 * ty);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const float y = b[r * pitch<D>() + tx + 16 * c];
+      acc[0][c] = fmaf(x.x, y, acc[0][c]);
+      acc[1][c] = fmaf(x.y, y, acc[1][c]);
+      acc[2][c] = fmaf(x.z, y, acc[2][c]);
+      acc[3][c] = fmaf(x.w, y, acc[3][c]);
+    }
+  }
+}
+
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct Params {
+  const float *q, *k, *v, *dO, *o;
+  const float *lse;       // backward
+  float *out, *out_lse;   // o, lse  |  dq
+  float *dk, *dv;         // partial sums [nsplit][bh][l][D]
+  float *delta;           // [bh][np]
+  const int32_t* act;
+  const uint4* bits;
+  int64_t np, l, bh;
+  int tiles, kv_heads, nsplit;
+  float scale;
+};
+
+// Half-tiles (64 states) of the batch entry: number, place and bits of the i-th.
+struct Halves {
+  const int32_t* list;
+  const uint4* bits;
+  int n;
+  int64_t l;
+  __device__ __forceinline__ Halves(const Params& P, int64_t bh) {
+    const int64_t b = bh / P.kv_heads;
+    list = P.act ? P.act + b * (P.tiles + 1) + 1 : nullptr;
+    bits = P.act ? P.bits + b * P.tiles : nullptr;
+    n = 2 * (P.act ? list[-1] : P.tiles);
+    l = P.l;
+  }
+  __device__ __forceinline__ int64_t at(int i, uint32_t& w0, uint32_t& w1) const {
+    const int t = list ? list[i >> 1] : i >> 1, h = i & 1;
+    uint32_t w[4];
+    if (bits) {
+      const uint4 b = bits[t];
+      w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
+    } else {
+      tail_words(l, t, w);
+    }
+    w0 = h ? w[2] : w[0];
+    w1 = h ? w[3] : w[1];
+    return (int64_t)t * kTile + h * kT;
+  }
+};
+
+__device__ __forceinline__ bool on(uint32_t w0, uint32_t w1, int j) {
+  return ((j < 32 ? w0 : w1) >> (j & 31)) & 1u;
+}
+}  // namespace xs
+
+template <int D>
+__global__ void __launch_bounds__(xs::kThreads) k_cross_fwd32(const xs::Params P) {
+  using namespace xs;
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm;
+  float* sk = sq + kT * pitch<D>();
+  float* sv = sk + kT * pitch<D>();
+  float* sp = sv + kT * pitch<D>();
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int64_t bh = blockIdx.y, row0 = (int64_t)blockIdx.x * kT;
+  const Halves H(P, bh);
+  load_tile<D>(sq, P.q + bh * P.np * D, row0, P.np, ~0u, ~0u);
+  float acc[4][D / 16], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+  }
+  const float sl2 = P.scale * kLog2e;
+  for (int h = 0; h < H.n; ++h) {
+    uint32_t w0, w1;
+    const int64_t at = H.at(h, w0, w1);
+    if (!(w0 | w1)) continue;
+    __syncthreads();
+    load_tile<D>(sk, P.k + bh * P.l * D, at, P.l, w0, w1);
+    load_tile<D>(sv, P.v + bh * P.l * D, at, P.l, w0, w1);
+    __syncthreads();
+    float s[4][4];
+    product<D>(sq, sk, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = on(w0, w1, tx + 16 * j) ? s[i][j] * sl2 : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+      const float mn = fmaxf(m[i], row_max(top));
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - base);
+        sum += p;
+        sp[(4 * ty + i) * kP + tx + 16 * j] = p;
+      }
+      l[i] = l[i] * f + row_sum(sum);
+      m[i] = mn;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) acc[i][c] *= f;
+    }
+    __syncwarp();  // a warp's rows of sp are its own
+    accumulate<D>(sp, sv, ty, tx, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 4 * ty + i;
+    if (row >= P.np) continue;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) P.out[(bh * P.np + row) * D + tx + 16 * c] = acc[i][c] * inv;
+    if (P.out_lse && tx == 0)
+      P.out_lse[bh * P.np + row] = l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
+  }
+}
+
+// delta_i = <dO_i, o_i>: 8 threads per row
+template <int D>
+__global__ void __launch_bounds__(256) k_cross_delta32(const xs::Params P) {
+  const int64_t row = blockIdx.x * 32ll + (threadIdx.x >> 3);
+  const int t = threadIdx.x & 7;
+  float s = 0.f;
+  if (row < P.bh * P.np)
+    for (int c = t * 4; c < D; c += 32) {
+      const float4 a = *reinterpret_cast<const float4*>(P.dO + row * D + c);
+      const float4 b = *reinterpret_cast<const float4*>(P.o + row * D + c);
+      s = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
+    }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (t == 0 && row < P.bh * P.np) P.delta[row] = s;
+}
+
+namespace xs {
+// Scores of a tile as probabilities (into sp, if any) and dS (into sd).
+template <int D>
+__device__ __forceinline__ void grads(const float* sq, const float* sg, const float* sk,
+                                      const float* sv, float* sp, float* sd, int ty, int tx,
+                                      const float (&nl)[4], const float (&dl)[4], uint32_t w0,
+                                      uint32_t w1, float scale) {
+  float s[4][4], g[4][4];
+  product<D>(sq, sk, ty, tx, s);
+  product<D>(sg, sv, ty, tx, g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = on(w0, w1, tx + 16 * j);
+      const float p = in ? exp2f(fmaf(s[i][j], scale * kLog2e, nl[i])) : 0.f;
+      const int at = (4 * ty + i) * kP + tx + 16 * j;
+      if (sp) sp[at] = p;
+      sd[at] = p * (g[i][j] - dl[i]) * scale;
+    }
+}
+}  // namespace xs
+
+template <int D>
+__global__ void __launch_bounds__(xs::kThreads) k_cross_dq32(const xs::Params P) {
+  using namespace xs;
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm;
+  float* sg = sq + kT * pitch<D>();
+  float* sk = sg + kT * pitch<D>();
+  float* sv = sk + kT * pitch<D>();
+  float* sd = sv + kT * pitch<D>();
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int64_t bh = blockIdx.y, row0 = (int64_t)blockIdx.x * kT;
+  const Halves H(P, bh);
+  load_tile<D>(sq, P.q + bh * P.np * D, row0, P.np, ~0u, ~0u);
+  load_tile<D>(sg, P.dO + bh * P.np * D, row0, P.np, ~0u, ~0u);
+  float acc[4][D / 16], nl[4], dl[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 4 * ty + i;
+    const bool in = row < P.np;
+    const float lse = in ? P.lse[bh * P.np + row] : -INFINITY;
+    nl[i] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    dl[i] = in ? P.delta[bh * P.np + row] : 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+  }
+  for (int h = 0; h < H.n; ++h) {
+    uint32_t w0, w1;
+    const int64_t at = H.at(h, w0, w1);
+    if (!(w0 | w1)) continue;
+    __syncthreads();
+    load_tile<D>(sk, P.k + bh * P.l * D, at, P.l, w0, w1);
+    load_tile<D>(sv, P.v + bh * P.l * D, at, P.l, w0, w1);
+    __syncthreads();
+    grads<D>(sq, sg, sk, sv, nullptr, sd, ty, tx, nl, dl, w0, w1, P.scale);
+    __syncwarp();
+    accumulate<D>(sd, sk, ty, tx, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 4 * ty + i;
+    if (row >= P.np) continue;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) P.out[(bh * P.np + row) * D + tx + 16 * c] = acc[i][c];
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(xs::kThreads) k_cross_dkv32(const xs::Params P) {
+  using namespace xs;
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm;
+  float* sg = sq + kT * pitch<D>();
+  float* sk = sg + kT * pitch<D>();
+  float* sv = sk + kT * pitch<D>();
+  float* sp = sv + kT * pitch<D>();
+  float* sd = sp + kT * kP;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int64_t bh = blockIdx.y;
+  const int half = blockIdx.x / P.nsplit, split = blockIdx.x % P.nsplit;
+  const int64_t at = (int64_t)half * kT;
+  uint32_t w[4];
+  if (P.act) {
+    const uint4 b = P.bits[bh / P.kv_heads * P.tiles + (half >> 1)];
+    w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
+  } else {
+    tail_words(P.l, half >> 1, w);
+  }
+  const uint32_t w0 = half & 1 ? w[2] : w[0], w1 = half & 1 ? w[3] : w[1];
+  load_tile<D>(sk, P.k + bh * P.l * D, at, P.l, w0, w1);
+  load_tile<D>(sv, P.v + bh * P.l * D, at, P.l, w0, w1);
+  float ak[4][D / 16], av[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
+  const int64_t qt = (P.np + kT - 1) / kT;
+  const int64_t t0 = qt * split / P.nsplit, t1 = (w0 | w1) ? qt * (split + 1) / P.nsplit : t0;
+  for (int64_t t = t0; t < t1; ++t) {
+    const int64_t row0 = t * kT;
+    __syncthreads();
+    load_tile<D>(sq, P.q + bh * P.np * D, row0, P.np, ~0u, ~0u);
+    load_tile<D>(sg, P.dO + bh * P.np * D, row0, P.np, ~0u, ~0u);
+    float nl[4], dl[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = row0 + 4 * ty + i;
+      const bool in = row < P.np;
+      const float lse = in ? P.lse[bh * P.np + row] : -INFINITY;
+      nl[i] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+      dl[i] = in ? P.delta[bh * P.np + row] : 0.f;
+    }
+    __syncthreads();
+    grads<D>(sq, sg, sk, sv, sp, sd, ty, tx, nl, dl, w0, w1, P.scale);
+    __syncthreads();
+    accumulate_t<D>(sp, sg, ty, tx, av);
+    accumulate_t<D>(sd, sq, ty, tx, ak);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = at + 4 * ty + i;
+    if (row >= P.l) continue;
+    const int64_t dst = ((split * P.bh + bh) * P.l + row) * D;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      P.dk[dst + tx + 16 * c] = ak[i][c];
+      P.dv[dst + tx + 16 * c] = av[i][c];
+    }
+  }
+}
+
+// out = sum over the ranges of part, in order
+__global__ void __launch_bounds__(256)
+    k_cross_sum32(const float* __restrict__ part, int nsplit, int64_t n, float* __restrict__ dk,
+                  const float* __restrict__ part2, float* __restrict__ dv) {
+  const int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 4;
+  if (i >= n) return;
+  const float* p = blockIdx.y ? part2 : part;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < nsplit; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(p + k * n + i);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  *reinterpret_cast<float4*>((blockIdx.y ? dv : dk) + i) = s;
+}
+
+static xs::Params simt_params(const Problem& p, const MaskTables& m) {
+  xs::Params P{};
+  P.q = static_cast<const float*>(p.q);
+  P.k = static_cast<const float*>(p.k);
+  P.v = static_cast<const float*>(p.v);
+  P.act = m.act;
+  P.bits = m.bits;
+  P.np = p.np;
+  P.l = p.l;
+  P.bh = p.bh;
+  P.tiles = (int)p.tiles();
+  P.kv_heads = p.kv_heads;
+  P.nsplit = 1;
+  P.scale = p.scale;
+  return P;
+}
+
+// Row ranges of the key gradients: enough blocks for two per SM.
+static int dkv_splits(const Problem& p) {
+  const int64_t blocks = p.bh * ((p.l + xs::kT - 1) / xs::kT), qt = (p.np + xs::kT - 1) / xs::kT;
+  int64_t n = (2 * (int64_t)sm_count() + blocks - 1) / (blocks > 0 ? blocks : 1);
+  if (n > qt) n = qt;
+  return n < 1 ? 1 : (int)n;
+}
+
+template <int D> static cudaError_t launch_fwd32(const Problem& p, xs::Params P) {
+  constexpr int bytes = 4 * (3 * xs::kT * xs::pitch<D>() + xs::kT * xs::kP);
+  static std::atomic<uint64_t> attr{0};
+  const cudaError_t e =
+      smem_attr_once(reinterpret_cast<const void*>(k_cross_fwd32<D>), bytes, attr);
+  if (e != cudaSuccess) return e;
+  k_cross_fwd32<D><<<dim3((unsigned)((p.np + xs::kT - 1) / xs::kT), (unsigned)p.bh), xs::kThreads,
+                     bytes, p.s>>>(P);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse) {
+  xs::Params P = simt_params(p, m);
+  P.out = static_cast<float*>(o);
+  P.out_lse = lse;
+  switch (p.d) {
+    case 48: return launch_fwd32<48>(p, P);
+    case 64: return launch_fwd32<64>(p, P);
+    case 96: return launch_fwd32<96>(p, P);
+    default: return launch_fwd32<128>(p, P);
+  }
+}
+
+size_t bwd_simt_bytes(const Problem& p) {
+  const size_t n = dkv_splits(p), e = (size_t)p.bh * p.l * p.d * sizeof(float);
+  return align256((size_t)p.bh * p.np * sizeof(float)) + (n > 1 ? 2 * align256(n * e) : 0);
+}
+
+template <int D> static cudaError_t launch_bwd32(const Problem& p, xs::Params P, float* dk, float* dv) {
+  constexpr int tile = xs::kT * xs::pitch<D>();
+  constexpr int bq = 4 * (4 * tile + xs::kT * xs::kP), bk = bq + 4 * xs::kT * xs::kP;
+  static std::atomic<uint64_t> aq{0}, ak{0};
+  cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(k_cross_dq32<D>), bq, aq);
+  if (e == cudaSuccess)
+    e = smem_attr_once(reinterpret_cast<const void*>(k_cross_dkv32<D>), bk, ak);
+  if (e != cudaSuccess) return e;
+  k_cross_delta32<D><<<(unsigned)((p.bh * p.np + 31) / 32), 256, 0, p.s>>>(P);
+  k_cross_dq32<D><<<dim3((unsigned)((p.np + xs::kT - 1) / xs::kT), (unsigned)p.bh), xs::kThreads,
+                    bq, p.s>>>(P);
+  const int64_t halves = (p.l + xs::kT - 1) / xs::kT;
+  k_cross_dkv32<D><<<dim3((unsigned)(halves * P.nsplit), (unsigned)p.bh), xs::kThreads, bk, p.s>>>(P);
+  count_launch(3);
+  if (P.nsplit > 1) {
+    const int64_t n = p.bh * p.l * D;
+    k_cross_sum32<<<dim3((unsigned)((n / 4 + 255) / 256), 2), 256, 0, p.s>>>(P.dk, P.nsplit, n, dk,
+                                                                           P.dv, dv);
+    count_launch();
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t bwd_simt(const Problem& p, const MaskTables& m, const void* o, const float* lse,
+                     const void* dO, void* dq, void* dk, void* dv, void* ws) {
+  xs::Params P = simt_params(p, m);
+  P.o = static_cast<const float*>(o);
+  P.dO = static_cast<const float*>(dO);
+  P.lse = lse;
+  P.out = static_cast<float*>(dq);
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  P.delta = reinterpret_cast<float*>(at);
+  at += align256((size_t)p.bh * p.np * sizeof(float));
+  P.nsplit = dkv_splits(p);
+  P.dk = static_cast<float*>(dk);
+  P.dv = static_cast<float*>(dv);
+  if (P.nsplit > 1) {
+    const size_t e = (size_t)P.nsplit * p.bh * p.l * p.d * sizeof(float);
+    P.dk = reinterpret_cast<float*>(at);
+    P.dv = reinterpret_cast<float*>(at + align256(e));
+  }
+  float *k = static_cast<float*>(dk), *v = static_cast<float*>(dv);
+  switch (p.d) {
+    case 48: return launch_bwd32<48>(p, P, k, v);
+    case 64: return launch_bwd32<64>(p, P, k, v);
+    case 96: return launch_bwd32<96>(p, P, k, v);
+    default: return launch_bwd32<128>(p, P, k, v);
+  }
+}
+
+}  // namespace xa
+}  // namespace p3d

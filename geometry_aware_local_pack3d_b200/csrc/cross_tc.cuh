@@ -1,0 +1,103 @@
+// Tensor-core building blocks of the cross-attention kernels: swizzled operand tiles that TMA
+// writes and tcgen05 reads.
+//
+// A tile of R rows x D bf16 lies in shared memory as D / CW blocks of R rows x CW elements, each
+// row of a block RB = 2 CW bytes (64 with the 64-byte swizzle; 32 with the 32-byte one where D is
+// no multiple of 32): one TMA box per block. The 16-byte pieces of 8 consecutive rows are permuted
+// so that both the K-major reads (rows = M or N) and the MN-major reads (rows = K) of an 8 x 16
+// byte core matrix touch 8 different bank groups. The same tile serves both kinds of read.
+#pragma once
+
+#include "cross.h"
+#include "tc.cuh"
+#include "tmap.h"
+#include "vec.cuh"
+
+namespace p3d {
+namespace xa {
+
+template <int D> struct Lay {
+  static constexpr int CW = D % 32 == 0 ? 32 : 16;
+  static constexpr int RB = 2 * CW;
+  static constexpr int NB = D / CW;
+  static constexpr int kSteps = D / 16;                    // K steps of a product over D
+  static constexpr int kPieces = RB / 16;                  // 16-byte pieces of a block's row
+  static constexpr uint64_t kType = RB == 64 ? 4ull : 6ull;  // 64-byte / 32-byte swizzle
+  static constexpr int bytes(int rows) { return rows * D * 2; }
+  // byte offset of 16-byte piece `pc` (of D / 8) of row r
+  __device__ __forceinline__ static int piece(int rows, int r, int pc) {
+    const int c = pc / kPieces, i = pc % kPieces;
+    const int x = RB == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
+    return c * rows * RB + r * RB + ((i ^ x) << 4);
+  }
+  // K-major operand (rows M or N, D contiguous): descriptor and the offset of K step ks
+  __device__ __forceinline__ static uint64_t kdesc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | ((uint64_t)(8 * RB >> 4) << 32) |
+           (1ull << 46) | (kType << 61);
+  }
+  __device__ __forceinline__ static constexpr uint64_t koff(int rows, int ks) {
+    return (uint64_t)(((ks * 32 / RB) * rows * RB + ks * 32 % RB) >> 4);
+  }
+  // MN-major operand (rows K, D = N contiguous): K step ks covers rows 16 ks .. 16 ks + 15
+  __device__ __forceinline__ static uint64_t mdesc(uint32_t addr, int rows) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(rows * RB >> 4) << 16) |
+           ((uint64_t)(8 * RB >> 4) << 32) | (1ull << 46) | (kType << 61);
+  }
+  __device__ __forceinline__ static constexpr uint64_t moff(int ks) {
+    return (uint64_t)((ks * 16 * RB) >> 4);
+  }
+};
+
+// [count][rows][d] bf16 as a 3D box source / target: boxes of CW elements x box_rows rows.
+template <int D>
+inline bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t count,
+                        int box_rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)count};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)rows * D * 2};
+  cuuint32_t box[3] = {(cuuint32_t)Lay<D>::CW, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            Lay<D>::RB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// All blocks of the tile that starts at row `row` of problem `p`.
+template <int D>
+__device__ __forceinline__ void load_rows(void* smem_dst, const CUtensorMap* map, int rows,
+                                          int64_t row, int p, uint64_t* bar) {
+#pragma unroll
+  for (int c = 0; c < Lay<D>::NB; ++c)
+    tc::tma_load_3d(static_cast<uint8_t*>(smem_dst) + c * rows * Lay<D>::RB, map, c * Lay<D>::CW,
+                    (int)row, p, bar);
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int x,
+                                             int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(tc::smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// the committed stores have read their shared memory / have completed
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace xa
+}  // namespace p3d

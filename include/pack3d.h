@@ -272,6 +272,104 @@ pack3d_status pack3d_attn_bwd_noalloc(const pack3d_index* idx, const void* q, co
                                       int kv_heads, float scale, uint32_t flags, void* dq,
                                       void* dk, void* dv, void* dgate, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The operators next to the PACK3D layer in a training step: cross attention of a field's tokens
+ * to states of another length, layer norm, and the global gradient norm with clipping. They need
+ * no index. The conventions above hold (dense row-major tensors, 16-byte aligned pointers unless
+ * stated otherwise, no allocation, errors before any launch); outputs must not overlap inputs
+ * unless stated otherwise. Calls share nothing but their arguments, so calls on different streams
+ * need different workspaces and nothing else.
+ * ---------------------------------------------------------------------------------------- */
+
+/* Bytes of workspace pack3d_cross_attn_fwd (backward 0) or pack3d_cross_attn_bwd (backward 1)
+ * needs on the current device; has_mask: whether a mask will be passed. 0 where none is needed,
+ * and where the arguments are invalid. Host-only. */
+size_t pack3d_cross_attn_workspace_bytes(int dtype, int batch, int heads, int kv_heads, int64_t n,
+                                         int64_t l, int head_dim, int has_mask, int backward);
+
+/* Cross attention: every row of q attends to the states (k, v) of its batch entry.
+ *   s_ij = scale <q_i, k_j>,  o_i = sum_j softmax_j(s_ij) v_j,  lse_i = log sum_j exp s_ij.
+ * q, o       device [B, H, N, d] dtype;  k, v device [B, H_kv, L, d] dtype (kv_heads as above).
+ * mask       device bytes [B, L], 0 leaves the state out; NULL: all take part. Nothing that a
+ *            state left out holds (infinities, NaN) reaches a result. A row with no state (an
+ *            empty mask, L = 0) has o = 0 and lse = -inf.
+ * n, l       rows and states, each 0 or more; (H / H_kv) n and l at most 2^30.
+ * head_dim   48, 64, 96 or 128.
+ * lse        device float32 [B, H, N] or NULL (natural logarithm; what the backward needs).
+ * workspace  device, 256-byte aligned, pack3d_cross_attn_workspace_bytes(..., 0) bytes (NULL where
+ *            that is 0); contents on entry are ignored. One call at a time may use it.
+ * status     device int32 word or NULL: a device-side wait that gives up records
+ *            PACK3D_ERR_TIMEOUT here if the word is 0 (an index's status word may be passed, or any
+ *            zeroed word; read it with pack3d_read_status).
+ * float32 runs on CUDA cores with 32-bit products, bfloat16 on tensor cores. */
+pack3d_status pack3d_cross_attn_fwd(const void* q, const void* k, const void* v,
+                                    const uint8_t* mask, int dtype, int batch, int heads,
+                                    int kv_heads, int64_t n, int64_t l, int head_dim, float scale,
+                                    void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                    int32_t* status, void* stream);
+
+/* Gradients of sum(dO * o) of pack3d_cross_attn_fwd. o, lse: the forward's results for the same
+ * q, k, v, mask and scale. dq [B, H, N, d], dk, dv [B, H_kv, L, d] dtype (a KV head's gradients
+ * sum over its query heads; those of a state left out are 0). workspace: as in the forward, of
+ * pack3d_cross_attn_workspace_bytes(..., 1) bytes. Results do not change from run to run. */
+pack3d_status pack3d_cross_attn_bwd(const void* q, const void* k, const void* v,
+                                    const uint8_t* mask, const void* o, const float* lse,
+                                    const void* dO, int dtype, int batch, int heads, int kv_heads,
+                                    int64_t n, int64_t l, int head_dim, float scale, void* dq,
+                                    void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                                    int32_t* status, void* stream);
+
+/* Reads (after synchronising `stream`) and clears a status word: OK, or the first error that a
+ * kernel recorded in it. */
+pack3d_status pack3d_read_status(int32_t* status, void* stream);
+
+/* Layer norm over the last dimension: y = (x - mu) / sqrt(var + eps) * weight + bias, mu and var
+ * the mean and (biased) variance of the row in float32.
+ * x, y          device [rows, cols] dtype, rows 0 or more, cols 1 or more (any length: a [B, H, N,
+ *               d] tensor is B H N rows of d).
+ * weight, bias  device [cols] of wdtype (element-aligned), or NULL for 1 and 0.
+ * eps           0 or more, finite.
+ * mean, rstd    device float32 [rows] or NULL: mu and 1 / sqrt(var + eps), what the backward
+ *               needs. */
+pack3d_status pack3d_layer_norm_fwd(const void* x, const void* weight, const void* bias, int dtype,
+                                    int wdtype, int64_t rows, int32_t cols, float eps, void* y,
+                                    float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace pack3d_layer_norm_bwd needs when it returns dweight or dbias. Host-only; 0
+ * if the arguments are invalid. */
+size_t pack3d_layer_norm_bwd_workspace_bytes(int dtype, int64_t rows, int32_t cols);
+
+/* Gradients of sum(dy * y): dx [rows, cols] dtype, and dweight, dbias [cols] of wdtype, each of
+ * the two NULL if not wanted. mean, rstd: the forward's. workspace: device, 16-byte aligned, of
+ * pack3d_layer_norm_bwd_workspace_bytes bytes (may be NULL when neither dweight nor dbias is
+ * wanted); contents on entry are ignored. Results do not change from run to run. */
+pack3d_status pack3d_layer_norm_bwd(const void* dy, const void* x, const void* weight,
+                                    const float* mean, const float* rstd, int dtype, int wdtype,
+                                    int64_t rows, int32_t cols, void* dx, void* dweight,
+                                    void* dbias, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* Bytes of workspace the two calls below need for n_tensors tensors. Host-only. */
+size_t pack3d_grad_norm_workspace_bytes(int n_tensors);
+
+/* norm = sqrt(sum over the tensors of the sum of squares), as one float32.
+ * grads, counts, dtypes  HOST arrays of n_tensors (0 or more): device pointer (aligned to its
+ *            element; may be NULL where the count is 0), number of elements, dtype of each.
+ * norm       device float32 [1].
+ * workspace  device, 16-byte aligned; contents on entry are ignored.
+ * The host arrays are read before the call returns. */
+pack3d_status pack3d_grad_norm(const void* const* grads, const int64_t* counts, const int* dtypes,
+                               int n_tensors, float* norm, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* As pack3d_grad_norm, and outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)). outs[i] may be
+ * grads[i] (clipped in place); any other overlap among the tensors written, or of one written with
+ * one read, is INVALID_ARG. A norm that is infinite or NaN scales as the formula says. */
+pack3d_status pack3d_clip_grad_norm(const void* const* grads, void* const* outs,
+                                    const int64_t* counts, const int* dtypes, int n_tensors,
+                                    float max_norm, float* norm, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* Reads (after synchronising `stream`) and clears the index's device status word: OK, or
  * the first device-detected error (DUP_COORD, COORD_RANGE, TIMEOUT). */
 pack3d_status pack3d_device_status(const pack3d_index* idx, void* stream);
