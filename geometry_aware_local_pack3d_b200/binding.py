@@ -404,53 +404,66 @@ _CODES = {torch.float32: PACK3D_F32, torch.bfloat16: PACK3D_BF16}
 
 def _here(t):
     """Whether t's device is the current one (the library launches on the current device)."""
-    return t.device.index == torch.cuda.current_device()
+    return t.get_device() == torch.cuda.current_device()
 
 
-def _stream_of(t, stream):
-    """The CUDA stream handle the call runs on: `stream`, or the current one of t's device."""
-    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+def _stream_of(index, stream):
+    """The CUDA stream handle the call runs on: `stream`, or the current one of device `index`."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _new(stream, *shape, dtype, device):
-    """An uninitialised tensor that belongs to the stream the call runs on, so that the caching
-    allocator cannot hand its memory out while the call's kernels still use it."""
+def _new(stream, like, shape, dtype):
+    """An uninitialised tensor on like's device that belongs to the stream the call runs on, so
+    that the caching allocator cannot hand its memory out while the call's kernels still use it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _need(t, what, shape, dtype, device):
+def _new_like(stream, like):
+    if stream is None:
+        return torch.empty_like(like)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(like)
+
+
+def _need(t, what, shape, dtype, index):
+    """shape None: any. index: the device's."""
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"PACK3D tensors must be contiguous CUDA tensors ({what})")
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{what} is {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
 
 
-def _workspace(workspace, need, stream, device):
+def _code(t):
+    code = _CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code  # raises for other types
+
+
+def _workspace(workspace, need, stream, like):
     if workspace is None:
-        return _new(stream, need, dtype=torch.uint8, device=device)
-    if (not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device
-            or workspace.dtype != torch.uint8):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        return _new(stream, like, (need,), torch.uint8)
+    if (not workspace.is_cuda or not workspace.is_contiguous()
+            or workspace.get_device() != like.get_device() or workspace.dtype != torch.uint8):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
     return workspace
 
 
-def _status_ptr(status, device):
+def _status_ptr(status, index):
     if status is None:
         return None
     if isinstance(status, Index):
-        if status.buf.device != device:
-            raise ValueError(f"the index is on {status.buf.device}, expected {device}")
+        if status.buf.get_device() != index:
+            raise ValueError(f"the index is on {status.buf.device}, expected cuda:{index}")
         return status.struct.status
-    if status.numel() < 1 or not status.is_contiguous() or status.device != device \
-            or status.dtype != torch.int32:
-        raise ValueError(f"status must be an Index or a contiguous int32 tensor on {device}")
+    if not status.is_cuda or status.numel() < 1 or not status.is_contiguous() \
+            or status.get_device() != index or status.dtype != torch.int32:
+        raise ValueError(f"status must be an Index or a contiguous int32 tensor on cuda:{index}")
     return status.data_ptr()
 
 
@@ -458,18 +471,20 @@ def _cross_shapes(q, k, v, mask):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q is [B, H, N, d], k and v are [B, H_kv, L, d]")
     B, H, N, d = q.shape
-    kv_shape = (B, k.shape[1], k.shape[2], d)
-    code = _dtype_code(q)
-    _need(q, "q", q.shape, q.dtype, q.device)
-    _need(k, "k", kv_shape, q.dtype, q.device)
-    _need(v, "v", kv_shape, q.dtype, q.device)
-    if k.shape[1] == 0:
+    _, HK, L, _ = k_shape = k.shape
+    code, dt, index = _code(q), q.dtype, q.get_device()
+    _need(q, "q", None, dt, index)
+    if k_shape != (B, HK, L, d):
+        raise ValueError(f"k has shape {tuple(k_shape)}, expected {(B, HK, L, d)}")
+    _need(k, "k", None, dt, index)
+    _need(v, "v", k_shape, dt, index)
+    if HK == 0:
         raise ValueError("k has no heads")
     if mask is not None:
         if mask.dtype != torch.bool and mask.dtype != torch.uint8:
             raise TypeError(f"mask is {mask.dtype}, expected torch.bool or torch.uint8")
-        _need(mask, "mask", (B, k.shape[2]), mask.dtype, q.device)
-    return B, H, k.shape[1], N, k.shape[2], d, code
+        _need(mask, "mask", (B, L), mask.dtype, index)
+    return B, H, HK, N, L, d, code, index
 
 
 def pack3d_cross_attn_workspace_bytes(dtype_code, batch, heads, kv_heads, n, l, head_dim,
@@ -484,30 +499,29 @@ def pack3d_cross_attn_fwd(q, k, v, *, mask=None, scale=None, o=None, lse=None,
     entry. mask: bool or uint8 [B, L], false leaves a state out (whatever it holds). Returns a dict
     with o and lse (lse when save_for_backward or when a buffer is passed; a row with no state has
     o = 0, lse = -inf). status: an Index or an int32 word for a timed-out device-side wait."""
-    B, H, HK, N, L, d, code = _cross_shapes(q, k, v, mask)
+    B, H, HK, N, L, d, code, index = _cross_shapes(q, k, v, mask)
     if not _here(q):
         with torch.cuda.device(q.device):
             return pack3d_cross_attn_fwd(q, k, v, mask=mask, scale=scale, o=o, lse=lse,
                                          save_for_backward=save_for_backward,
                                          workspace=workspace, status=status, stream=stream)
-    dev = q.device
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if o is None:
-        o = _new(stream, B, H, N, d, dtype=q.dtype, device=dev)
+        o = _new_like(stream, q)
     else:
-        _need(o, "o", q.shape, q.dtype, dev)
+        _need(o, "o", q.shape, q.dtype, index)
     if lse is not None:
-        _need(lse, "lse", (B, H, N), torch.float32, dev)
+        _need(lse, "lse", (B, H, N), torch.float32, index)
     elif save_for_backward:
-        lse = _new(stream, B, H, N, dtype=torch.float32, device=dev)
+        lse = _new(stream, q, (B, H, N), torch.float32)
     L_ = lib()
     need = L_.pack3d_cross_attn_workspace_bytes(code, B, H, HK, N, L, d, mask is not None, 0)
-    ws = _workspace(workspace, need, stream, dev) if need else None
+    ws = _workspace(workspace, need, stream, q) if need else None
     st = L_.pack3d_cross_attn_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), None if mask is None else mask.data_ptr(), code,
         B, H, HK, N, L, d, scale, o.data_ptr(), None if lse is None else lse.data_ptr(),
         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-        _status_ptr(status, dev), _stream_of(q, stream))
+        _status_ptr(status, index), _stream_of(index, stream))
     if st != PACK3D_OK:
         raise Pack3DError(st, "pack3d_cross_attn_fwd")
     return dict(o=o, lse=lse)
@@ -517,30 +531,27 @@ def pack3d_cross_attn_bwd(q, k, v, saved, dO, *, mask=None, scale=None, workspac
                           status=None, stream=None):
     """Gradients dq, dk, dv of sum(dO * o). saved: the dict returned by
     pack3d_cross_attn_fwd(save_for_backward=True) for the same q, k, v, mask and scale."""
-    B, H, HK, N, L, d, code = _cross_shapes(q, k, v, mask)
+    B, H, HK, N, L, d, code, index = _cross_shapes(q, k, v, mask)
     if not _here(q):
         with torch.cuda.device(q.device):
             return pack3d_cross_attn_bwd(q, k, v, saved, dO, mask=mask, scale=scale,
                                          workspace=workspace, status=status, stream=stream)
-    dev = q.device
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     o, lse = saved["o"], saved["lse"]
     if lse is None:
         raise ValueError("the forward was run without save_for_backward")
-    _need(o, "o", q.shape, q.dtype, dev)
-    _need(dO, "dO", q.shape, q.dtype, dev)
-    _need(lse, "lse", (B, H, N), torch.float32, dev)
-    dq = _new(stream, B, H, N, d, dtype=q.dtype, device=dev)
-    dk = _new(stream, B, HK, L, d, dtype=q.dtype, device=dev)
-    dv = _new(stream, B, HK, L, d, dtype=q.dtype, device=dev)
+    _need(o, "o", q.shape, q.dtype, index)
+    _need(dO, "dO", q.shape, q.dtype, index)
+    _need(lse, "lse", (B, H, N), torch.float32, index)
+    dq, dk, dv = _new_like(stream, q), _new_like(stream, k), _new_like(stream, v)
     L_ = lib()
     need = L_.pack3d_cross_attn_workspace_bytes(code, B, H, HK, N, L, d, mask is not None, 1)
-    ws = _workspace(workspace, need, stream, dev) if need else None
+    ws = _workspace(workspace, need, stream, q) if need else None
     st = L_.pack3d_cross_attn_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), None if mask is None else mask.data_ptr(),
         o.data_ptr(), lse.data_ptr(), dO.data_ptr(), code, B, H, HK, N, L, d, scale,
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if ws is None else ws.data_ptr(),
-        0 if ws is None else ws.numel(), _status_ptr(status, dev), _stream_of(q, stream))
+        0 if ws is None else ws.numel(), _status_ptr(status, index), _stream_of(index, stream))
     if st != PACK3D_OK:
         raise Pack3DError(st, "pack3d_cross_attn_bwd")
     return dict(dq=dq, dk=dk, dv=dv)
@@ -548,19 +559,20 @@ def pack3d_cross_attn_bwd(q, k, v, saved, dO, *, mask=None, scale=None, workspac
 
 def pack3d_read_status(status, stream=None):
     """Reads (after synchronising the stream) and clears an int32 status word."""
+    index = status.get_device()
     with torch.cuda.device(status.device):
-        return int(lib().pack3d_read_status(_status_ptr(status, status.device),
-                                            _stream_of(status, stream)))
+        return int(lib().pack3d_read_status(_status_ptr(status, index),
+                                            _stream_of(index, stream)))
 
 
-def _norm_params(x, weight, bias):
-    """Type code of weight and bias (one type; float32 when neither is given)."""
+def _norm_params(cols, index, *params):
+    """Type of weight and bias (one type; float32 when neither is given)."""
     wtype = None
-    for t, what in ((weight, "weight"), (bias, "bias")):
+    for t in params:
         if t is not None:
             wtype = wtype or t.dtype
-            _need(t, what, (x.shape[-1],), wtype, x.device)
-            _dtype_code(t)
+            _code(t)
+            _need(t, "weight or bias", (cols,), wtype, index)
     return wtype or torch.float32
 
 
@@ -568,30 +580,30 @@ def pack3d_layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None,
                           save_for_backward=False, stream=None):
     """Layer norm over the last dimension of x. weight, bias: [cols], float32 or bfloat16, or None.
     Returns a dict with y and, with save_for_backward, the rows' mean and rstd (float32)."""
-    code = _dtype_code(x)
-    if x.dim() < 1 or x.shape[-1] < 1:
+    code, index, shape = _code(x), x.get_device(), x.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("x needs a last dimension of one or more elements")
-    _need(x, "x", x.shape, x.dtype, x.device)
+    _need(x, "x", None, x.dtype, index)
     if not _here(x):
         with torch.cuda.device(x.device):
             return pack3d_layer_norm_fwd(x, weight, bias, eps=eps, y=y,
                                          save_for_backward=save_for_backward, stream=stream)
-    dev, cols = x.device, x.shape[-1]
+    cols = shape[-1]
     rows = x.numel() // cols
-    wtype = _norm_params(x, weight, bias)
+    wtype = _norm_params(cols, index, weight, bias)
     if y is None:
-        y = _new(stream, *x.shape, dtype=x.dtype, device=dev)
+        y = _new_like(stream, x)
     else:
-        _need(y, "y", x.shape, x.dtype, dev)
+        _need(y, "y", shape, x.dtype, index)
     mean = rstd = None
     if save_for_backward:
-        mean = _new(stream, *x.shape[:-1], dtype=torch.float32, device=dev)
-        rstd = _new(stream, *x.shape[:-1], dtype=torch.float32, device=dev)
+        mean = _new(stream, x, shape[:-1], torch.float32)
+        rstd = _new_like(stream, mean)
     st = lib().pack3d_layer_norm_fwd(
         x.data_ptr(), None if weight is None else weight.data_ptr(),
         None if bias is None else bias.data_ptr(), code, _CODES[wtype], rows, cols, eps,
         y.data_ptr(), None if mean is None else mean.data_ptr(),
-        None if rstd is None else rstd.data_ptr(), _stream_of(x, stream))
+        None if rstd is None else rstd.data_ptr(), _stream_of(index, stream))
     if st != PACK3D_OK:
         raise Pack3DError(st, "pack3d_layer_norm_fwd")
     return dict(y=y, mean=mean, rstd=rstd)
@@ -601,50 +613,50 @@ def pack3d_layer_norm_bwd(dy, x, weight, saved, *, weight_grad=True, bias_grad=T
                           workspace=None, stream=None):
     """Gradients of sum(dy * y): dx and, where wanted, dweight and dbias (of weight's type; float32
     without a weight). saved: the dict returned by pack3d_layer_norm_fwd(save_for_backward=True)."""
-    code = _dtype_code(x)
-    _need(x, "x", x.shape, x.dtype, x.device)
+    code, index, shape = _code(x), x.get_device(), x.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError("x needs a last dimension of one or more elements")
+    _need(x, "x", None, x.dtype, index)
     if not _here(x):
         with torch.cuda.device(x.device):
             return pack3d_layer_norm_bwd(dy, x, weight, saved, weight_grad=weight_grad,
                                          bias_grad=bias_grad, workspace=workspace, stream=stream)
-    dev, cols = x.device, x.shape[-1]
+    cols = shape[-1]
     rows = x.numel() // cols
-    wtype = _norm_params(x, weight, None)
+    wtype = _norm_params(cols, index, weight)
     mean, rstd = saved["mean"], saved["rstd"]
     if mean is None or rstd is None:
         raise ValueError("the forward was run without save_for_backward")
-    _need(dy, "dy", x.shape, x.dtype, dev)
-    _need(mean, "mean", x.shape[:-1], torch.float32, dev)
-    _need(rstd, "rstd", x.shape[:-1], torch.float32, dev)
-    dx = _new(stream, *x.shape, dtype=x.dtype, device=dev)
-    dw = _new(stream, cols, dtype=wtype, device=dev) if weight_grad else None
-    db = _new(stream, cols, dtype=wtype, device=dev) if bias_grad else None
+    _need(dy, "dy", shape, x.dtype, index)
+    _need(mean, "mean", shape[:-1], torch.float32, index)
+    _need(rstd, "rstd", shape[:-1], torch.float32, index)
+    dx = _new_like(stream, x)
+    dw = _new(stream, x, (cols,), wtype) if weight_grad else None
+    db = _new(stream, x, (cols,), wtype) if bias_grad else None
     L_ = lib()
     ws = None
     if weight_grad or bias_grad:
         ws = _workspace(workspace, L_.pack3d_layer_norm_bwd_workspace_bytes(code, rows, cols),
-                        stream, dev)
+                        stream, x)
     st = L_.pack3d_layer_norm_bwd(
         dy.data_ptr(), x.data_ptr(), None if weight is None else weight.data_ptr(),
         mean.data_ptr(), rstd.data_ptr(), code, _CODES[wtype], rows, cols, dx.data_ptr(),
         None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-        _stream_of(x, stream))
+        _stream_of(index, stream))
     if st != PACK3D_OK:
         raise Pack3DError(st, "pack3d_layer_norm_bwd")
     return dict(dx=dx, dweight=dw, dbias=db)
 
 
-def _tensor_list(ts, what, device):
-    """Host arrays (addresses, lengths, type codes) of a list of tensors."""
-    if not all([t.is_contiguous() and t.device == device for t in ts]):
-        raise ValueError(f"{what} must be contiguous tensors on {device}")
-    try:
-        codes = array.array("i", [_CODES[t.dtype] for t in ts])
-    except KeyError as e:
-        raise TypeError(f"PACK3D supports float32 and bfloat16 tensors, got {e.args[0]}") from None
-    return (array.array("Q", [t.data_ptr() for t in ts]),
-            array.array("q", [t.numel() for t in ts]), codes)
+_T = torch.Tensor
+
+
+def _tensor_list(ts, what, index):
+    """Lengths, types and addresses of a list of tensors, each checked."""
+    if not all(map(_T.is_contiguous, ts)) or any([i != index for i in map(_T.get_device, ts)]):
+        raise ValueError(f"{what} must be contiguous CUDA tensors on cuda:{index}")
+    return list(map(_T.numel, ts)), [t.dtype for t in ts], array.array("Q", map(_T.data_ptr, ts))
 
 
 def _address(a):
@@ -660,7 +672,7 @@ def pack3d_grad_norm(grads, *, norm=None, workspace=None, stream=None, device=No
 def pack3d_clip_grad_norm(grads, max_norm, *, outs=None, norm=None, workspace=None, stream=None,
                           device=None):
     """Scales every tensor in `grads` by min(1, max_norm / (norm + 1e-6)), norm being their
-    pack3d_grad_norm, in place or into `outs` (a list of tensors of the same shapes and types).
+    pack3d_grad_norm, in place or into `outs` (a list of tensors of the same lengths and types).
     Returns the norm before clipping."""
     return _grads("pack3d_clip_grad_norm", grads, True, outs, max_norm, norm, workspace, stream,
                   device)
@@ -668,36 +680,42 @@ def pack3d_clip_grad_norm(grads, max_norm, *, outs=None, norm=None, workspace=No
 
 def _grads(call, grads, clip, outs, max_norm, norm, workspace, stream, device):
     grads = list(grads)
-    dev = torch.device(grads[0].device if grads else device if device is not None else "cuda")
-    if dev.type != "cuda":
+    if grads:
+        like = grads[0]
+    else:
+        like = torch.empty(0, device="cuda" if device is None else device)
+    if not like.is_cuda:
         raise ValueError("PACK3D tensors must be contiguous CUDA tensors")
-    if dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _grads(call, grads, clip, outs, max_norm, norm, workspace, stream, dev)
-    ptrs, counts, codes = _tensor_list(grads, "grads", dev)
+    index = like.get_device()
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _grads(call, grads, clip, outs, max_norm, norm, workspace, stream, like.device)
+    counts, dtypes, ptrs = _tensor_list(grads, "grads", index)
+    try:
+        codes = array.array("i", [_CODES[t] for t in dtypes])
+    except KeyError as e:
+        raise TypeError(f"PACK3D supports float32 and bfloat16 tensors, got {e.args[0]}") from None
     n = len(grads)
+    to = ptrs
+    if outs is not None:
+        to_counts, to_dtypes, to = _tensor_list(list(outs), "outs", index)
+        if to_counts != counts or to_dtypes != dtypes:
+            raise ValueError("outs must match grads in number, lengths and types")
+    counts = array.array("q", counts)
     if norm is None:
-        norm = _new(stream, 1, dtype=torch.float32, device=dev)
+        norm = _new(stream, like, (1,), torch.float32)
     else:
-        _need(norm, "norm", (1,), torch.float32, dev)
+        _need(norm, "norm", (1,), torch.float32, index)
     L_ = lib()
-    ws = _workspace(workspace, L_.pack3d_grad_norm_workspace_bytes(n), stream, dev)
-    s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-    if not clip:
-        st = L_.pack3d_grad_norm(_address(ptrs), _address(counts), _address(codes), n,
-                                 norm.data_ptr(), ws.data_ptr(), ws.numel(), s)
-    else:
-        to = ptrs
-        if outs is not None:
-            outs = list(outs)
-            to, to_counts, to_codes = _tensor_list(outs, "outs", dev)
-            if to_counts != counts or to_codes != codes:
-                raise ValueError("outs must match grads in length, sizes and types")
+    ws = _workspace(workspace, L_.pack3d_grad_norm_workspace_bytes(n), stream, like)
+    s = _stream_of(index, stream)
+    if clip:
         st = L_.pack3d_clip_grad_norm(_address(ptrs), _address(to), _address(counts),
                                       _address(codes), n, float(max_norm), norm.data_ptr(),
                                       ws.data_ptr(), ws.numel(), s)
+    else:
+        st = L_.pack3d_grad_norm(_address(ptrs), _address(counts), _address(codes), n,
+                                 norm.data_ptr(), ws.data_ptr(), ws.numel(), s)
     if st != PACK3D_OK:
         raise Pack3DError(st, call)
     return norm
