@@ -24,24 +24,40 @@ struct Problem {
   int64_t tiles() const { return (l + kTile - 1) / kTile; }
 };
 
-// Tables of the mask, built by k_cross_mask in the workspace: for each batch entry, the tiles of
-// 128 states that hold an unmasked one (act: their number, then their indices in order) and one
-// bit per state (bits: four words per tile; states past L count as masked).
+// Tables of the mask, built by k_cross_mask in the workspace: one bit per state (bits: a run of
+// words per batch entry, states past L count as masked) and, for tiles of 32 tw states, the tiles
+// that hold an unmasked one (act: their number, then their indices in order).
 struct MaskTables {
-  int32_t* act;  // [B][tiles + 1]; null: no mask
-  uint4* bits;   // [B][tiles]
+  int32_t* act;    // [B][tiles + 1]; null: no mask
+  uint32_t* bits;  // [B][words]
+  int tw, tiles;   // words per tile; tiles
+  int64_t words;   // words per batch entry, a multiple of 12: whole tiles of 2, 3 and 4 words
 };
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-inline size_t mask_bytes(const Problem& p) {
-  return align256(sizeof(int32_t) * p.batch * (p.tiles() + 1)) +
-         align256(sizeof(uint4) * p.batch * p.tiles());
+inline MaskTables mask_at(const Problem& p, int tw, void* ws) {
+  MaskTables m{};
+  m.tw = tw;
+  m.tiles = (int)((p.l + 32 * tw - 1) / (32 * tw));
+  m.words = ((p.l + 31) / 32 + 11) / 12 * 12;
+  if (p.mask) {
+    m.act = static_cast<int32_t*>(ws);
+    m.bits = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) +
+                                         align256(sizeof(int32_t) * p.batch * (m.tiles + 1)));
+  }
+  return m;
 }
-inline MaskTables mask_at(const Problem& p, void* ws) {
-  if (!p.mask) return MaskTables{nullptr, nullptr};
-  uint8_t* at = static_cast<uint8_t*>(ws);
-  return MaskTables{reinterpret_cast<int32_t*>(at),
-                    reinterpret_cast<uint4*>(
-                        at + align256(sizeof(int32_t) * p.batch * (p.tiles() + 1)))};
+inline size_t mask_bytes(const Problem& p, int tw) {
+  const MaskTables m = mask_at(p, tw, nullptr);
+  return align256(sizeof(int32_t) * p.batch * (m.tiles + 1)) +
+         align256(sizeof(uint32_t) * p.batch * m.words);
+}
+
+// States per tile of the forward on tensor cores: two buffers of S (one at d = 128), P (bf16, half
+// as many columns) and O of a row tile take half of the 512 columns of TMEM.
+constexpr int fwd_tile(int) { return 64; }
+// Words per tile of the mask's list, forward and backward.
+inline int mask_tile_words(const Problem& p, bool backward) {
+  return !backward && p.dtype == PACK3D_BF16 ? fwd_tile(p.d) / 32 : kTile / 32;
 }
 
 cudaError_t build_mask(const Problem& p, const MaskTables& m);
@@ -58,17 +74,25 @@ size_t bwd_simt_bytes(const Problem& p);
 cudaError_t bwd_simt(const Problem& p, const MaskTables& m, const void* o, const float* lse,
                      const void* dO, void* dq, void* dk, void* dv, void* ws);
 
-// Does state j of the tile whose words are `w` take part?
-__device__ __forceinline__ bool state_bit(const uint32_t (&w)[4], int j) {
-  return (w[j >> 5] >> (j & 31)) & 1u;
-}
-// The words of tile `tile` without a mask: the states before L.
-__device__ __forceinline__ void tail_words(int64_t l, int tile, uint32_t (&w)[4]) {
+// The W words of states from `at` on: of the batch entry's bits, or the states before L.
+template <int W>
+__device__ __forceinline__ void state_words(const uint32_t* bits, int64_t l, int64_t at,
+                                            uint32_t (&w)[W]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t left = l - (int64_t)tile * kTile - 32 * i;
-    w[i] = left >= 32 ? 0xffffffffu : (left <= 0 ? 0u : (1u << left) - 1u);
+  for (int i = 0; i < W; ++i) {
+    if (bits) {
+      w[i] = bits[(at >> 5) + i];
+    } else {
+      const int64_t left = l - at - 32 * i;
+      w[i] = left >= 32 ? 0xffffffffu : (left <= 0 ? 0u : (1u << left) - 1u);
+    }
   }
+}
+template <int W> __device__ __forceinline__ bool all_states(const uint32_t (&w)[W]) {
+  uint32_t a = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < W; ++i) a &= w[i];
+  return a == 0xffffffffu;
 }
 
 }  // namespace xa

@@ -57,7 +57,7 @@ size_t bytes_of(const xa::Problem& p, bool mask, bool backward) {
   const bool tc = p.dtype == PACK3D_BF16;
   const size_t own = backward ? (tc ? xa::bwd_tc_bytes(p) : xa::bwd_simt_bytes(p))
                               : (tc ? xa::fwd_tc_bytes(p) : 0);
-  return own + (mask ? xa::mask_bytes(p) : 0);
+  return own + (mask ? xa::mask_bytes(p, xa::mask_tile_words(p, backward)) : 0);
 }
 
 pack3d_status check_workspace(const xa::Problem& p, const void* ws, size_t bytes, bool backward) {
@@ -68,8 +68,8 @@ pack3d_status check_workspace(const xa::Problem& p, const void* ws, size_t bytes
   return bytes < need ? PACK3D_ERR_WORKSPACE : PACK3D_OK;
 }
 
-void* after_mask(const xa::Problem& p, void* ws) {
-  return p.mask ? static_cast<uint8_t*>(ws) + xa::mask_bytes(p) : ws;
+void* after_mask(const xa::Problem& p, int tw, void* ws) {
+  return p.mask ? static_cast<uint8_t*>(ws) + xa::mask_bytes(p, tw) : ws;
 }
 }  // namespace
 
@@ -109,10 +109,11 @@ extern "C" pack3d_status pack3d_cross_attn_fwd(const void* q, const void* k, con
   if (l == 0)
     return cuda_status(empty_rows(o, rows * p.d * (dtype == PACK3D_BF16 ? 2 : 4), lse, rows, p.s));
   if ((st = check_workspace(p, workspace, workspace_bytes, false)) != PACK3D_OK) return st;
-  const xa::MaskTables m = xa::mask_at(p, workspace);
+  const int tw = xa::mask_tile_words(p, false);
+  const xa::MaskTables m = xa::mask_at(p, tw, workspace);
   cudaError_t e = xa::build_mask(p, m);
   if (e == cudaSuccess)
-    e = dtype == PACK3D_BF16 ? xa::fwd_tc(p, m, o, lse, after_mask(p, workspace))
+    e = dtype == PACK3D_BF16 ? xa::fwd_tc(p, m, o, lse, after_mask(p, tw, workspace))
                              : xa::fwd_simt(p, m, o, lse);
   return cuda_status(e);
 }
@@ -153,9 +154,10 @@ extern "C" pack3d_status pack3d_cross_attn_bwd(const void* q, const void* k, con
     return cuda_status(e);
   }
   if ((st = check_workspace(p, workspace, workspace_bytes, true)) != PACK3D_OK) return st;
-  const xa::MaskTables m = xa::mask_at(p, workspace);
+  const int tw = xa::mask_tile_words(p, true);
+  const xa::MaskTables m = xa::mask_at(p, tw, workspace);
   cudaError_t e = xa::build_mask(p, m);
-  void* ws = after_mask(p, workspace);
+  void* ws = after_mask(p, tw, workspace);
   if (e == cudaSuccess)
     e = dtype == PACK3D_BF16 ? xa::bwd_tc(p, m, o, lse, dO, dq, dk, dv, ws)
                              : xa::bwd_simt(p, m, o, lse, dO, dq, dk, dv, ws);

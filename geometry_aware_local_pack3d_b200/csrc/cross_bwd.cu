@@ -43,10 +43,10 @@ __device__ __forceinline__ float2 f2(uint32_t a, uint32_t b) {
 struct Params {
   const float2* rows;  // [bh][npad]
   const int32_t* act;
-  const uint4* bits;
+  const uint32_t* bits;
   int32_t* status;
   long long budget;
-  int64_t np, npad, l, bh, units;
+  int64_t np, npad, l, bh, units, words;
   int rtiles, tiles, kv_heads, nsplit;
   float scale, scale_log2;
   __nv_bfloat16 *dk, *dv;   // written when nsplit is 1
@@ -111,7 +111,7 @@ struct Unit {
   int64_t bh, row0;
   int n;
   const int32_t* list;
-  const uint4* bits;
+  const uint32_t* bits;
   __device__ __forceinline__ Unit(const xb::Params& P, int64_t u) {
     bh = u / P.rtiles;
     row0 = (u % P.rtiles) * kTile;
@@ -121,7 +121,7 @@ struct Unit {
     n = (int)((P.l + xb::kHalf - 1) / xb::kHalf);
     if (P.act) {
       list = P.act + b * (P.tiles + 1) + 1;
-      bits = P.bits + b * P.tiles;
+      bits = P.bits + b * P.words;
       n = 2 * list[-1];
     }
   }
@@ -129,15 +129,7 @@ struct Unit {
     return list ? (int64_t)list[j >> 1] * kTile + (j & 1) * xb::kHalf : (int64_t)j * xb::kHalf;
   }
   __device__ __forceinline__ void words(int64_t l, int j, uint32_t (&w)[2]) const {
-    if (bits) {
-      const uint2 b = reinterpret_cast<const uint2*>(bits)[2 * list[j >> 1] + (j & 1)];
-      w[0] = b.x;
-      w[1] = b.y;
-    } else {
-      const int64_t left = l - (int64_t)j * xb::kHalf;
-      w[0] = left >= 32 ? ~0u : (1u << left) - 1u;
-      w[1] = left >= 64 ? ~0u : (left <= 32 ? 0u : (1u << (left - 32)) - 1u);
-    }
+    state_words(bits, l, at(j), w);
   }
 };
 }  // namespace xq
@@ -435,12 +427,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
   const int kt = (int)((item / P.nsplit) % P.tiles);
   const int64_t bh = item / ((int64_t)P.nsplit * P.tiles);
   uint32_t w[4];
-  if (P.act) {
-    const uint4 b = P.bits[bh / P.kv_heads * P.tiles + kt];
-    w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
-  } else {
-    tail_words(P.l, kt, w);
-  }
+  state_words(P.act ? P.bits + bh / P.kv_heads * P.words : nullptr, P.l, (int64_t)kt * kTile, w);
   const bool any = (w[0] | w[1] | w[2] | w[3]) != 0u;
   const int64_t steps = (P.np + xb::kHalf - 1) / xb::kHalf;
   const int64_t i0 = steps * split / P.nsplit;
@@ -722,6 +709,7 @@ static cudaError_t launch_bwd(const Problem& p, const MaskTables& m, const void*
   P.bh = p.bh;
   P.rtiles = (int)(npad / kTile);
   P.tiles = (int)p.tiles();
+  P.words = m.words;
   P.kv_heads = p.kv_heads;
   P.scale = p.scale;
   P.scale_log2 = p.scale * kLog2e;

@@ -3,20 +3,29 @@
 //   s_ij = tau <q_i, k_j>,  p = softmax over the unmasked states j,  o_i = sum_j p_ij v_j,
 //   lse_i = log sum_j exp s_ij;   a row with no unmasked state has o = 0, lse = -inf.
 //
-// Work unit: 256 rows of one problem = two 128-row tiles that share every K and V tile of 128
-// states. Persistent CTAs; warps 0-3 and 4-7 are the softmax and epilogue of tile 0 and 1 (thread
-// = row = TMEM lane), warp 8 loads by TMA, warps 9 and 10 issue the MMAs of tile 0 and 1, warp 11
-// clears the masked rows of V. Per state tile: S = q K^T (fp32 in TMEM), the softmax threads write
-// P = 2^(s - m) in bf16 over S, O += P V (P read from TMEM). The two tiles' chains S -> P -> O are
-// independent, so that one tile's products run under the other's softmax.
+// Work unit: 256 rows of one problem = two 128-row tiles that share every K and V tile of KT states
+// (96, or 64 at d = 128: see fwd_tile). Persistent CTAs of 18 warps:
+//   0-3, 4-7  softmax of tile 0 and 1 (thread = row = TMEM lane)
+//   8-11      epilogue of both tiles: O / sum in bf16, through the tile's consumed q rows, by TMA
+//   12        TMA loads;  13, 14  S products of tile 0 and 1;  15, 16  O products of them
+//   17        clears the masked rows of V
+// Per state tile: S = q K^T (fp32 in TMEM); the softmax threads read S into registers and hand its
+// columns back at once, so that the next tile's S is formed under this tile's exponentials;
+// P = 2^(s - m) in bf16 goes to columns of its own and O += P V (P read from TMEM).
+// What bounds it: the exponentials (16 a cycle and SM, 1,536 cycles per 256 x 96 scores against
+// 1,224 of tensor work). A warp alone keeps its sub-partition's exponential unit busy half the time
+// (it waits for S, takes maxima, packs, stores); four warps per sub-partition cover for one another.
 // The running reference m of a row moves only when its maximum has grown by more than 2^8 (p is at
 // most 2^8 and its sum and O are fp32, so nothing overflows and no digits are lost); O is then
-// rescaled in TMEM, which few tiles need after the first.
+// rescaled in TMEM, which few tiles need after the first. The two threads of a row exchange their
+// maxima through shared memory once per tile, and their sums once per unit.
 // P is rounded to bf16 for the second product (relative 2^-9, as the output itself); the row sum is
 // taken from the unrounded values.
 // Masked states: their S is replaced by -inf whatever it holds, and their V rows (which may hold
 // NaN) are zeroed in shared memory, in the tiles that mix masked and unmasked states; tiles without
 // an unmasked state are not in the list and are never loaded.
+// A context of one tile stays in shared memory while its problem lasts: the CTAs then take runs of
+// consecutive units, and only the rows move.
 // When there are fewer units than SMs and several state tiles, the states are split over nsplit
 // CTAs; each writes its normalised fp32 rows and lse, and k_cross_join adds them with the weights
 // exp(lse_s - lse).
@@ -29,25 +38,38 @@ namespace p3d {
 namespace xa {
 
 namespace xf {
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;  // whole groups of four warps (two warps idle): they split registers
+// Registers of a thread at launch, and of the softmax warps and the others once they have split the
+// block's.
+constexpr int kRegs = 96, kMore = 144, kLess = 64;
+static_assert(256 * kMore + (kThreads - 256) * kLess <= kThreads * kRegs, "registers of the block");
 constexpr int kSmemLimit = 232448;
 template <int D> struct Smem {
-  static constexpr int TB = Lay<D>::bytes(kTile);
-  static constexpr int kQ = 0;                       // [2 buffers][2 tiles]
-  static constexpr int kRing = 4 * TB;
-  static constexpr int kFit = (kSmemLimit - 2048 - kRing) / TB;
-  static constexpr int kSlots = kFit < 8 ? kFit : 8; // K and V tiles take turns
-  static constexpr int kBar = kRing + kSlots * TB;
-  static constexpr int kBytes = kBar + 512 + 1024;   // + room to align the base to 1,024
+  static constexpr int KT = fwd_tile(D);               // states per tile
+  static constexpr int QB = Lay<D>::bytes(kTile), KB = Lay<D>::bytes(KT);
+  static constexpr int kSum = 0;                       // [2 turns][2 tiles][128] row sums
+  static constexpr int kRef = kSum + 2048;             // the same of the references
+  static constexpr int kQ = kRef + 2048;               // [2 buffers][2 tiles]
+  static constexpr int kRing = kQ + 4 * QB;
+  static constexpr int kFit = (kSmemLimit - 1024 - 512 - kRing) / KB;
+  static constexpr int kSlots = kFit < 8 ? kFit : 8;   // K and V tiles take turns
+  static constexpr int kBar = kRing + kSlots * KB;
+  static constexpr int kBytes = kBar + 512 + 1024;     // + room to align the base to 1,024
+  // TMEM columns of tile t: S, P, O at t * 256 + ...
+  static constexpr int kBufs = D <= 96 ? 2 : 1;        // of S
+  static constexpr uint32_t kS = 0, kP = kBufs * KT, kO = kP + KT / 2;
+  static_assert(kO + D <= 256, "tensor memory of a tile");
+  static_assert(kSlots >= 4, "two K and two V tiles");
 };
-// barriers
 constexpr int kMaxSlots = 8;
 // V tiles the row-clearing warp may be ahead of the MMA warps: fewer than the ring holds
 constexpr int kReady = 8;
 enum {
   B_QFULL = 0, B_QEMPTY = 4, B_FULL = 8, B_EMPTY = B_FULL + kMaxSlots,
-  B_READY = B_EMPTY + kMaxSlots, B_SFULL = B_READY + kReady, B_PFULL = B_SFULL + 2,
-  B_DONE = B_PFULL + 2, B_STAGED = B_DONE + 2, B_DRAIN = B_STAGED + 2, B_COUNT = B_DRAIN + 2
+  B_READY = B_EMPTY + kMaxSlots, B_SFULL = B_READY + kReady, B_SFREE = B_SFULL + 4,
+  B_PFULL = B_SFREE + 4, B_DONE = B_PFULL + 2, B_SUM = B_DONE + 2,
+  B_OFULL = B_SUM + 4, B_OFREE = B_OFULL + 2, B_STAGED = B_OFREE + 2, B_DRAIN = B_STAGED + 2,
+  B_COUNT = B_DRAIN + 4
 };
 static_assert(8 * B_COUNT + 16 <= 512, "barrier area");
 
@@ -57,38 +79,81 @@ struct Params {
   float* part_o;     // [nsplit][bh][np][D], split launches
   float* part_lse;   // [nsplit][bh][np]
   const int32_t* act;
-  const uint4* bits;
+  const uint32_t* bits;
   int32_t* status;
   long long budget;
-  int64_t np, l, bh, units;
-  int pairs, tiles, kv_heads, nsplit;
+  int64_t np, l, bh, words;
+  int units, pairs, tiles, kv_heads, nsplit;
+  int step_pr, step_bh;  // pairs and problems from one unit of a CTA to its next
+  int resident;      // one state tile: K and V stay while the problem lasts
   float scale_log2;
 };
 
-// A unit's place: problem, first row, and its range [j0, j1) of the batch entry's list of tiles.
-struct Unit {
-  int64_t bh, row0;
-  int split, j0, j1;
-  const int32_t* list;  // null: tile j is j
-  const uint4* bits;
-  bool two;             // has rows for the second tile
-  __device__ __forceinline__ Unit(const Params& P, int64_t u) {
-    split = (int)(u % P.nsplit);
-    const int64_t r = u / P.nsplit;
-    bh = r / P.pairs;
-    row0 = (r % P.pairs) * (2 * kTile);
-    two = row0 + kTile < P.np;
-    const int64_t b = bh / P.kv_heads;
-    int n = P.tiles;
+// The units of a CTA in order: every gridDim-th, or a run of consecutive ones. A unit is a pair of
+// row tiles of one problem, with its range [j0, j1) of the batch entry's list of state tiles.
+struct Units {
+  int left;              // units still to come, this one included
+  int bh, pr, split, j0, j1;
+  const int32_t* list;   // null: tile j is j
+  const uint32_t* bits;
+  bool fresh;            // the problem's first unit here
+  __device__ __forceinline__ explicit Units(const Params& P) {
+    const uint32_t b = blockIdx.x, g = gridDim.x, n = P.units;
+    uint32_t first = b;
+    if (P.resident) {
+      const uint32_t per = n / g, more = n - per * g;
+      first = b * per + min(b, more);
+      left = (int)(per + (b < more ? 1 : 0));
+    } else {
+      left = (int)((n - b + g - 1) / g);
+    }
+    split = 0;
+    if (P.nsplit > 1) {  // (the units are then at most the CTAs: one each)
+      split = (int)(first % (uint32_t)P.nsplit);
+      first /= (uint32_t)P.nsplit;
+    }
+    bh = (int)(first / (uint32_t)P.pairs);
+    pr = (int)(first - (uint32_t)bh * P.pairs);
+    fresh = true;
+    place(P);
+  }
+  __device__ __forceinline__ void place(const Params& P) {
     list = nullptr;
     bits = nullptr;
+    j0 = 0;
+    j1 = P.tiles;
     if (P.act) {
-      list = P.act + b * (P.tiles + 1) + 1;
-      n = list[-1];
-      bits = P.bits + b * P.tiles;
+      const int b = (int)((uint32_t)bh / (uint32_t)P.kv_heads);
+      list = P.act + (int64_t)b * (P.tiles + 1) + 1;
+      j1 = left > 0 ? list[-1] : 0;
+      bits = P.bits + b * P.words;
     }
-    j0 = (int)((int64_t)n * split / P.nsplit);
-    j1 = (int)((int64_t)n * (split + 1) / P.nsplit);
+    if (P.nsplit > 1) {
+      // (below 2^32: at most 2^24 tiles and kMaxSplits ranges)
+      const uint32_t n = (uint32_t)j1;
+      j0 = (int)(n * (uint32_t)split / (uint32_t)P.nsplit);
+      j1 = (int)(n * (uint32_t)(split + 1) / (uint32_t)P.nsplit);
+    }
+  }
+  __device__ __forceinline__ void next(const Params& P) {
+    --left;
+    const int was = bh;
+    pr += P.step_pr;
+    bh += P.step_bh;
+    if (pr >= P.pairs) {
+      pr -= P.pairs;
+      ++bh;
+    }
+    fresh = bh != was;
+    if (P.act && fresh) place(P);
+  }
+  __device__ __forceinline__ bool any() const { return j0 != j1; }
+  __device__ __forceinline__ int64_t row0() const { return (int64_t)pr * (2 * kTile); }
+  __device__ __forceinline__ bool two(const Params& P) const { return row0() + kTile < P.np; }
+  // the unit's state tiles are loaded for it, and given back after it
+  __device__ __forceinline__ bool loads(const Params& P) const { return !P.resident || fresh; }
+  __device__ __forceinline__ bool releases(const Params& P) const {
+    return !P.resident || left == 1 || pr + 1 == P.pairs;
   }
   __device__ __forceinline__ int tile(int j) const { return list ? list[j] : j; }
 };
@@ -102,7 +167,8 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
   using namespace xf;
   using S = Smem<D>;
   using Ly = Lay<D>;
-  constexpr int NS = S::kSlots;
+  constexpr int NS = S::kSlots, KT = S::KT, KW = KT / 32;
+  constexpr int kEpi = 8, kLoad = 12, kMma = 13, kClear = 17;  // first warp of each role
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -110,7 +176,8 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kBar + 8 * B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kBar + 8 * B_COUNT + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  tc::Abort ab{abort_flag, P.status, P.budget};
+  const Waiter ab{abort_flag, P.budget};
+  const uint32_t sb = tc::smem_u32(bars);  // barrier i at sb + 8 i
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&bars[B_QFULL + i], 1);
@@ -122,331 +189,428 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
     }
     for (int i = 0; i < kReady; ++i) tc::mbar_init(&bars[B_READY + i], 1);
     for (int t = 0; t < 2; ++t) {
-      tc::mbar_init(&bars[B_SFULL + t], 1);
+      for (int b = 0; b < 4; b += 2) {  // a barrier per buffer of S: they run one ahead
+        tc::mbar_init(&bars[B_SFULL + b + t], 1);
+        tc::mbar_init(&bars[B_SFREE + b + t], 128);
+      }
       tc::mbar_init(&bars[B_PFULL + t], 128);
       tc::mbar_init(&bars[B_DONE + t], 1);
+      tc::mbar_init(&bars[B_SUM + t], 128);      // a barrier per turn: the softmax may be two
+      tc::mbar_init(&bars[B_SUM + 2 + t], 128);  // units ahead of the epilogue
+      tc::mbar_init(&bars[B_OFULL + t], 1);
+      tc::mbar_init(&bars[B_OFREE + t], 128);
       tc::mbar_init(&bars[B_STAGED + t], 128);
       tc::mbar_init(&bars[B_DRAIN + t], 1);
+      tc::mbar_init(&bars[B_DRAIN + 2 + t], 1);
     }
     abort_flag[0] = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 9) tc::tmem_alloc(tmem_slot, 512);
+  if (warp == kMma) tc::tmem_alloc(tmem_slot, 512);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
-  if (warp < 8) {
-    // ------------------------------------------------------------ softmax and epilogue
-    // a row's 128 logits stay in registers: 2 x 128 x 208 + 128 x 88 = 384 x 168
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int t = warp >> 2, wt = warp & 3;
-    const int rin = wt * 32 + lane;
-    const uint32_t tl = tbase + ((uint32_t)(wt * 32) << 16);
-    const uint32_t ts = tl + 128u * t, to = tl + 256u + 128u * t;
-    uint32_t gc = 0, uc = 0, staged = 0;  // state tiles, units and stores this tile has had
+  if (warp < kEpi) {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMore));
+    const int t = warp >> 2;
+    const int rin = (warp & 3) * 32 + lane;
+    const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16) + 256u * t;
+    const uint32_t tp = tl + S::kP, to = tl + S::kO;
+    uint32_t gc = 0, uc = 0;  // state tiles and units this row tile has had
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
-      const Unit U(P, u);
-      if (t == 1 && !U.two) continue;
-      const int64_t row = U.row0 + t * kTile + rin;
-      const int64_t grow = U.bh * P.np + row;
-      const bool valid = row < P.np;
-      const bool busy = row - lane < P.np;  // the warp has a row at all
-      if (U.j0 == U.j1) {
-        // no state takes part: zeros
-        if (valid) {
-          if (P.nsplit > 1) {
-            P.part_lse[U.split * P.bh * P.np + grow] = -INFINITY;
-          } else {
-            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(P.o + grow * D + e) = z;
-            if (P.lse) P.lse[grow] = -INFINITY;
-          }
+    for (Units U(P); U.left > 0 && ok; U.next(P)) {
+      if ((t == 1 && !U.two(P)) || !U.any()) continue;
+      if (U.row0() + t * kTile + (warp & 3) * 32 >= P.np) {
+        // the warp has no row: nothing to compute, but it follows every phase of the barriers
+        for (int j = U.j0; j < U.j1; ++j, ++gc) {
+          const int b = gc % S::kBufs;
+          ok = ab.all(sb + 8 * (B_SFULL + 2 * b + t), gc / S::kBufs);
+          if (!ok) break;
+          arrive32(sb + 8 * (B_SFREE + 2 * b + t));
+          if (gc) ok = ab.all(sb + 8 * (B_DONE + t), gc - 1);
+          if (!ok) break;
+          if (j + 1 == U.j1) arrive32(sb + 8 * (B_SUM + 2 * (uc & 1) + t));
+          arrive32(sb + 8 * (B_PFULL + t));
         }
+        ++uc;
         continue;
       }
       float m = -INFINITY, lsum = 0.f;  // reference (in powers of two) and sum
-      uint4 nb = U.bits ? U.bits[U.tile(U.j0)] : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t seen = 0;  // the next S was there when the tile before looked
+#pragma unroll 1
       for (int j = U.j0; j < U.j1; ++j, ++gc) {
-        uint32_t w[4] = {nb.x, nb.y, nb.z, nb.w};
-        if (!U.bits) tail_words(P.l, j, w);
-        if (U.bits && j + 1 < U.j1) nb = U.bits[U.tile(j + 1)];
-        if (!__all_sync(0xffffffffu, ab.wait(&bars[B_SFULL + t], gc & 1))) { ok = false; break; }
-        if (busy) {
+        const int b = gc % S::kBufs;
+        const uint32_t ts = tl + S::kS + b * KT;
+        ok = ab.all(seen, sb + 8 * (B_SFULL + 2 * b + t), gc / S::kBufs);
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (U.bits || j + 1 == P.tiles) {
+          // the masked logits become -inf whatever they hold
+          uint32_t w[KW];
+          state_words(U.bits, P.l, (int64_t)U.tile(j) * KT, w);
+          if (!all_states(w)) {
+#pragma unroll 1
+            for (int h = 0; h < KW; ++h) {
+              const uint32_t wh = h == 0 ? w[0] : w[KW - 1];
+              uint32_t s[32];
+              tc::tmem_ld32(ts + 32 * h, s);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[c] = ((wh >> c) & 1u) ? s[c] : 0xff800000u;
+              tc::tmem_st16(ts + 32 * h, reinterpret_cast<uint32_t(&)[16]>(s[0]));
+              tc::tmem_st16(ts + 32 * h + 16, reinterpret_cast<uint32_t(&)[16]>(s[16]));
+            }
+            tc::tmem_wait_st();
+          }
+        }
+        uint32_t s[KT];
+#pragma unroll
+        for (int c = 0; c < KT; c += 32)
+          tc::tmem_ld32(ts + c, reinterpret_cast<uint32_t(&)[32]>(s[c]));
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
+        arrive32(sb + 8 * (B_SFREE + 2 * b + t));
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < KT; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx[i] = tc::max3f(mx[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
+        const bool up = top > m + 8.f;
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? ex2(m - top) : 1.f;
+          lsum *= f;
+          if (up) m = top;
+          // (first tile: O holds nothing of this unit, and the first product overwrites it)
+          if (j > U.j0) {
+            ok = ab.all(sb + 8 * (B_DONE + t), gc - 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16(to + c, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc::tmem_st16(to + c, o);
+            }
+          }
+        }
+        const float nm = m == -INFINITY ? 0.f : -m;
+        const float2 sl2 = make_float2(P.scale_log2, P.scale_log2), nm2 = make_float2(nm, nm);
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t pk[KT / 2], done = 0;
+#pragma unroll
+        for (int c = 0; c < KT; c += 2) {
+          if (c == KT - 16) {
+            // looked at here, used below
+            done = ab.probe(sb + 8 * (B_DONE + t), gc - 1);
+            const int nb = (gc + 1) % S::kBufs;
+            seen = ab.probe(sb + 8 * (B_SFULL + 2 * nb + t), (gc + 1) / S::kBufs);
+          }
+          const float2 x =
+              tc::fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2, nm2);
+          const float2 p = make_float2(ex2(x.x), ex2(x.y));
+          sum = tc::add2(sum, p);
+          pk[c >> 1] = tc::pack_bf16(p.x, p.y);
+        }
+        lsum += sum.x + sum.y;
+        // O and the columns of P are the previous tile's until its product has completed
+        if (gc) {
+          ok = ab.all(done, sb + 8 * (B_DONE + t), gc - 1);
+          if (!ok) break;
           tc::tc_fence_after();
-          uint32_t s[2][64];
-          tc::tmem_ld64(ts, s[0]);
-          tc::tmem_ld64(ts + 64, s[1]);
-          tc::tmem_wait_ld();
-          if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              s[c >> 6][c & 63] = ((w[c >> 5] >> (c & 31)) & 1u) ? s[c >> 6][c & 63] : 0xff800000u;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < 128; c += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mx[i] = tc::max3f(mx[i], __uint_as_float(s[c >> 6][(c & 63) + 2 * i]),
-                                __uint_as_float(s[c >> 6][(c & 63) + 2 * i + 1]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
-          const bool grow_m = top > m + 8.f;
-          if (__any_sync(0xffffffffu, grow_m)) {
-            // no earlier tile: O holds nothing yet and the first product overwrites it
-            const float f = grow_m ? ex2(m - top) : 1.f;
-            lsum *= f;
-            if (grow_m) m = top;
-            if (j > U.j0) {
-#pragma unroll
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tc::tmem_ld16(to + c, o);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tc::tmem_st16(to + c, o);
-              }
-            }
-          }
-          const float nm = m == -INFINITY ? 0.f : -m;
-          const float2 sl2 = make_float2(P.scale_log2, P.scale_log2), nm2 = make_float2(nm, nm);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int c = 32 * h + 2 * i;
-              const float2 x = tc::fma2(make_float2(__uint_as_float(s[c >> 6][c & 63]),
-                                                    __uint_as_float(s[c >> 6][(c & 63) + 1])),
-                                        sl2, nm2);
-              const float2 p = make_float2(ex2(x.x), ex2(x.y));
-              sum[i & 1] = tc::add2(sum[i & 1], p);
-              pk[i] = tc::pack_bf16(p.x, p.y);
-            }
-            tc::tmem_st16(ts + 16 * h, pk);
-          }
-          lsum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          tc::tmem_wait_st();
-          tc::tc_fence_before();
         }
-        tc::mbar_arrive(&bars[B_PFULL + t]);
-      }
-      if (!ok) break;
-      if (!__all_sync(0xffffffffu, ab.wait(&bars[B_DONE + t], (gc - 1) & 1))) break;
-      tc::tc_fence_after();
-      const float inv = lsum > 0.f ? 1.f / lsum : (lsum == 0.f ? 0.f : lsum);
-      const float le = lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * kLn2;
-      const int buf = uc & 1;
-      if (P.nsplit > 1) {
-        const int64_t at = U.split * P.bh * P.np + grow;
-        if (valid) P.part_lse[at] = le;
 #pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tc::tmem_ld16(to + c, o);
-          tc::tmem_wait_ld();
-          if (valid) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(P.part_o + at * D + c + i) = make_float4(
-                  __uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                  __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-          }
-        }
+        for (int c = 0; c < KT / 2; c += 16)
+          tc::tmem_st16(tp + c, reinterpret_cast<uint32_t(&)[16]>(pk[c]));
+        tc::tmem_wait_st();
         tc::tc_fence_before();
-        if (rin == 0) tc::mbar_arrive(&bars[B_QEMPTY + 2 * buf + t]);
-      } else {
-        // the tile's q rows have been consumed: their buffer takes the output rows
-        uint8_t* stage = smem + S::kQ + (2 * buf + t) * S::TB;
-        if (valid && P.lse) P.lse[grow] = le;
-#pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tc::tmem_ld16(to + c, o);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              pk[i] = tc::pack_bf16(__uint_as_float(o[8 * h + 2 * i]) * inv,
-                                    __uint_as_float(o[8 * h + 2 * i + 1]) * inv);
-            *reinterpret_cast<uint4*>(stage + Ly::piece(kTile, rin, c / 8 + h)) =
-                make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          }
+        if (j + 1 == U.j1) {
+          // The row's sum and reference go to the epilogue. Its reads of this turn's slots two
+          // units ago came before the product that the wait above saw complete; and this arrival
+          // comes before the last P's, so that none can belong to the next unit's phase.
+          reinterpret_cast<float*>(smem + S::kSum)[(uc & 1) * 256 + t * 128 + rin] = lsum;
+          reinterpret_cast<float*>(smem + S::kRef)[(uc & 1) * 256 + t * 128 + rin] = m;
+          arrive32(sb + 8 * (B_SUM + 2 * (uc & 1) + t));
         }
-        tc::tc_fence_before();
-        tc::fence_proxy_async_smem();
-        tc::mbar_arrive(&bars[B_STAGED + t]);
-        if (rin == 0) {
-          // an aborting warp may never arrive: the wait is bounded as the others
-          if (!ab.wait(&bars[B_STAGED + t], staged++ & 1)) ok = false;
-#pragma unroll
-          for (int c = 0; c < Ly::NB && ok; ++c)
-            tma_store_3d(&mo, stage + c * kTile * Ly::RB, c * Ly::CW, (int)(U.row0 + t * kTile),
-                         (int)U.bh);
-          bulk_commit();
-          bulk_wait_read();
-          tc::mbar_arrive(&bars[B_QEMPTY + 2 * buf + t]);
-        }
-        ok = __all_sync(0xffffffffu, ok);  // a warp leaves the loop as one
+        arrive32(sb + 8 * (B_PFULL + t));
       }
+      tc::tmem_wait_ld();  // (an aborted run leaves no load of S in flight)
       ++uc;
     }
-    if (rin == 0) bulk_wait();
   } else {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-   if (warp == 8) {
-    // ------------------------------------------------------------ TMA loads
-    if (lane == 0) {
-      tc::tma_prefetch_desc(&mq);
-      tc::tma_prefetch_desc(&mk);
-      tc::tma_prefetch_desc(&mv);
-      uint32_t kv = 0, uc[2] = {0, 0};
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLess));
+    if (warp < kLoad) {
+      // ---------------------------------------------------------- epilogue
+      const int rin = (warp & 3) * 32 + lane;
+      uint32_t uc[2] = {0, 0};
       bool ok = true;
-      for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
-        const Unit U(P, u);
-        if (U.j0 == U.j1) continue;
-        for (int t = 0; t < (U.two ? 2 : 1) && ok; ++t, ++uc[t - 1]) {
-          const int i = 2 * (uc[t] & 1) + t;
-          if (uc[t] >= 2 && !ab.wait(&bars[B_QEMPTY + i], ((uc[t] >> 1) - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc::mbar_expect_tx(&bars[B_QFULL + i], S::TB);
-          load_rows<D>(smem + S::kQ + i * S::TB, &mq, kTile, U.row0 + t * kTile, (int)U.bh,
-                       &bars[B_QFULL + i]);
-        }
-        for (int j = U.j0; j < U.j1 && ok; ++j) {
-          const int64_t at = (int64_t)U.tile(j) * kTile;
-          for (int x = 0; x < 2; ++x, ++kv) {
-            const int st = kv % NS;
-            if (kv >= (uint32_t)NS && !ab.wait(&bars[B_EMPTY + st], ((kv / NS) - 1) & 1)) {
+      for (Units U(P); U.left > 0 && ok; U.next(P)) {
+        const int nt = U.two(P) ? 2 : 1;
+#pragma unroll 1
+        for (int t = 0; t < nt && ok; ++t) {
+          const int64_t row = U.row0() + t * kTile + rin;
+          const int64_t grow = U.bh * P.np + row;
+          const bool valid = row < P.np, part = P.nsplit > 1;
+          const int64_t at = U.split * P.bh * P.np + grow;
+          const bool any = U.any();
+          const uint32_t turn = (t ? uc[1] : uc[0]) & 1;
+          float inv = 0.f, le = -INFINITY;  // a row without any state: zeros
+          if (any) {
+            if (!ab.all(sb + 8 * (B_SUM + 2 * turn + t), (t ? uc[1] : uc[0]) >> 1) ||
+                !ab.all(sb + 8 * (B_OFULL + t), turn)) {
               ok = false;
               break;
             }
-            tc::mbar_expect_tx(&bars[B_FULL + st], S::TB);
-            load_rows<D>(smem + S::kRing + st * S::TB, x ? &mv : &mk, kTile, at, (int)U.bh,
-                         &bars[B_FULL + st]);
+            tc::tc_fence_after();
+            const int slot = turn * 256 + t * 128 + rin;
+            const float lsum = reinterpret_cast<const float*>(smem + S::kSum)[slot];
+            const float m = reinterpret_cast<const float*>(smem + S::kRef)[slot];
+            if (lsum != 0.f) {
+              inv = lsum > 0.f ? 1.f / lsum : lsum;
+              le = (m + log2f(lsum)) * kLn2;
+            }
+          }
+          if (valid) {
+            if (part)
+              P.part_lse[at] = le;
+            else if (P.lse)
+              P.lse[grow] = le;
+          }
+          if (part && !any) continue;  // the join skips it
+          // the tile's q rows have been consumed: their buffer takes the output rows
+          uint8_t* stage = smem + S::kQ + (2 * turn + t) * S::QB;
+          const uint32_t to = tbase + ((uint32_t)((warp & 3) * 32) << 16) + 256u * t + S::kO;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            if (any) {
+              tc::tmem_ld16(to + c, o);
+              tc::tmem_wait_ld();
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = any ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+            if (part) {
+              if (valid)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                  *reinterpret_cast<uint4*>(P.part_o + at * D + c + i) =
+                      make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              continue;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                pk[i] = tc::pack_bf16(__uint_as_float(o[8 * h + 2 * i]),
+                                      __uint_as_float(o[8 * h + 2 * i + 1]));
+              const uint4 v = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              if (any)
+                *reinterpret_cast<uint4*>(stage + Ly::piece(kTile, rin, c / 8 + h)) = v;
+              else if (valid)
+                *reinterpret_cast<uint4*>(P.o + grow * D + c + 8 * h) = v;
+            }
+          }
+          if (!any) continue;
+          tc::tc_fence_before();
+          // (staged before free: a thread a unit ahead of another cannot meet its phase)
+          tc::fence_proxy_async_smem();
+          if (!part) arrive32(sb + 8 * (B_STAGED + t));
+          arrive32(sb + 8 * (B_OFREE + t));
+          if (rin == 0) {
+            if (!part) {
+              // an aborting warp may never arrive: the wait is bounded as the others
+              if (!ab.wait(sb + 8 * (B_STAGED + t), turn)) ok = false;
+#pragma unroll 1
+              for (int c = 0; c < Ly::NB && ok; ++c)
+                tma_store_3d(&mo, stage + c * kTile * Ly::RB, c * Ly::CW,
+                             (int)(U.row0() + t * kTile), U.bh);
+              bulk_commit();
+              bulk_wait_read();
+            }
+            arrive32(sb + 8 * (B_QEMPTY + 2 * turn + t));
+          }
+          ok = __all_sync(0xffffffffu, ok);  // a warp leaves the loop as one
+          if (t) ++uc[1]; else ++uc[0];
+        }
+      }
+      if (rin == 0) bulk_wait();
+    } else if (warp == kLoad) {
+      // ---------------------------------------------------------- TMA loads
+      if (lane == 0) {
+        tc::tma_prefetch_desc(&mq);
+        tc::tma_prefetch_desc(&mk);
+        tc::tma_prefetch_desc(&mv);
+        uint32_t kv = 0, uc[2] = {0, 0};
+        bool ok = true;
+        for (Units U(P); U.left > 0 && ok; U.next(P)) {
+          if (!U.any()) continue;
+          const int nt = U.two(P) ? 2 : 1;
+#pragma unroll 1
+          for (int t = 0; t < nt && ok; ++t) {
+            const uint32_t n = t ? uc[1] : uc[0];
+            const int i = 2 * (n & 1) + t;
+            if (n >= 2) ok = ab.wait(sb + 8 * (B_QEMPTY + i), (n >> 1) - 1);
+            if (!ok) break;
+            tc::mbar_expect_tx(&bars[B_QFULL + i], S::QB);
+            load_rows<D>(smem + S::kQ + i * S::QB, &mq, kTile, U.row0() + t * kTile, U.bh,
+                         &bars[B_QFULL + i]);
+            if (t) ++uc[1]; else ++uc[0];
+          }
+          if (!U.loads(P)) continue;
+#pragma unroll 1
+          for (int j = 2 * U.j0; j < 2 * U.j1 && ok; ++j, ++kv) {
+            // K and V of a tile take turns
+            const int st = kv % NS;
+            if (kv >= (uint32_t)NS) ok = ab.wait(sb + 8 * (B_EMPTY + st), kv / NS - 1);
+            if (!ok) break;
+            tc::mbar_expect_tx(&bars[B_FULL + st], S::KB);
+            load_rows<D>(smem + S::kRing + st * S::KB, j & 1 ? &mv : &mk, KT,
+                         (int64_t)U.tile(j >> 1) * KT, U.bh, &bars[B_FULL + st]);
           }
         }
+        // an aborted run leaves no copy in flight
+        for (uint32_t k = kv > (uint32_t)NS ? kv - NS : 0; k < kv; ++k)
+          tc::mbar_wait(&bars[B_FULL + (k % NS)], (k / NS) & 1);
+        for (int t = 0; t < 2; ++t)
+          for (uint32_t k = uc[t] > 2 ? uc[t] - 2 : 0; k < uc[t]; ++k)
+            tc::mbar_wait(&bars[B_QFULL + 2 * (k & 1) + t], (k >> 1) & 1);
       }
-      // an aborted run leaves no copy in flight
-      for (uint32_t k = kv > (uint32_t)NS ? kv - NS : 0; k < kv; ++k)
-        tc::mbar_wait(&bars[B_FULL + (k % NS)], (k / NS) & 1);
-      for (int t = 0; t < 2; ++t)
-        for (uint32_t k = uc[t] > 2 ? uc[t] - 2 : 0; k < uc[t]; ++k)
-          tc::mbar_wait(&bars[B_QFULL + 2 * (k & 1) + t], (k >> 1) & 1);
+    } else if (warp < kMma + 2) {
+      // ---------------------------------------------------------- S products of tile t
+      // S needs only what the softmax threads have read, and is there when they come back for it
+      const int t = warp - kMma;
+      const uint32_t ts = __shfl_sync(0xffffffffu, tbase, 0) + 256u * t + S::kS;
+      const uint32_t id_s = tc::idesc_bf16_f32(128, KT, false, false);
+      const uint64_t qd0 = Ly::kdesc(tc::smem_u32(smem + S::kQ + t * S::QB));
+      const uint64_t kd0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
+      uint32_t kv = 0, n = 0, uc = 0;  // slot pairs given back; state tiles and units so far
+      bool ok = true;
+#pragma unroll 1
+      for (Units U(P); U.left > 0 && ok; U.next(P)) {
+        if (!U.any()) continue;
+        const bool mine = t == 0 || U.two(P), gives = U.releases(P);
+        if (mine) ok = ab.all(sb + 8 * (B_QFULL + 2 * (uc & 1) + t), uc >> 1);
+        const uint64_t qd = qd0 + ((2 * (uc & 1) * S::QB) >> 4);
+#pragma unroll 1
+        for (int j = U.j0; j < U.j1 && ok; ++j) {
+          const uint32_t st = (2 * kv) % NS, b = n % S::kBufs;
+          const uint32_t fb = sb + 8 * (B_FULL + st), eb = sb + 8 * (B_SFREE + 2 * b + t);
+          const bool wait = mine && n >= S::kBufs;
+          const uint32_t pf = ab.probe(fb, 2 * kv / NS);
+          const uint32_t pe = wait ? ab.probe(eb, n / S::kBufs - 1) : 1u;
+          ok = ab.all(pf, fb, 2 * kv / NS) && (!wait || ab.all(pe, eb, n / S::kBufs - 1));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            if (mine) {
+              const uint64_t kd = kd0 + ((st * S::KB) >> 4);
+#pragma unroll
+              for (int ks = 0; ks < Ly::kSteps; ++ks)
+                tc::mma_ss(ts + b * KT, qd + Ly::koff(kTile, ks), kd + Ly::koff(KT, ks), id_s,
+                           ks > 0);
+              commit32(sb + 8 * (B_SFULL + 2 * b + t));
+            }
+            if (gives) commit32(sb + 8 * (B_EMPTY + st));
+          }
+          __syncwarp();
+          n += mine;
+          kv += gives;
+        }
+        uc += mine;
+      }
+      if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN + t));
+      __syncwarp();
+      if (!tc::mbar_wait(&bars[B_DRAIN + t], 0, 100000000LL)) *abort_flag = 1;
+    } else if (warp < kClear) {
+      // ---------------------------------------------------------- O products of tile t
+      const int t = warp - kMma - 2;
+      const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0) + 256u * t;
+      const uint32_t tp = tb + S::kP, to = tb + S::kO;
+      const uint32_t id_o = tc::idesc_bf16_f32(128, D, false, true);
+      const uint64_t vd0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), KT);
+      const bool masked = P.act != nullptr;
+      uint32_t kv = 0, n = 0, uc = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (Units U(P); U.left > 0 && ok; U.next(P)) {
+        if (!U.any()) continue;
+        const bool mine = t == 0 || U.two(P), gives = U.releases(P);
+        // O still holds the previous unit's rows until the epilogue has read them
+        if (mine && uc) ok = ab.all(sb + 8 * (B_OFREE + t), uc - 1);
+#pragma unroll 1
+        for (int j = U.j0; j < U.j1 && ok; ++j) {
+          const uint32_t st = (2 * kv + 1) % NS;
+          const uint32_t vb = sb + 8 * (masked ? B_READY + kv % kReady : B_FULL + st);
+          const uint32_t vp = masked ? kv / kReady : (2 * kv + 1) / NS;
+          const uint32_t pv = ab.probe(vb, vp);
+          if (mine) ok = ab.all(sb + 8 * (B_PFULL + t), n);
+          ok = ok && ab.all(pv, vb, vp);
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            if (mine) {
+              const uint64_t vd = vd0 + ((st * S::KB) >> 4);
+#pragma unroll
+              for (int ks = 0; ks < KT / 16; ++ks)
+                tc::mma_ts(to, tp + ks * 8, vd + Ly::moff(ks), id_o, (j > U.j0 || ks > 0) ? 1u : 0u);
+              commit32(sb + 8 * (B_DONE + t));
+              if (j + 1 == U.j1) commit32(sb + 8 * (B_OFULL + t));
+            }
+            if (gives) commit32(sb + 8 * (B_EMPTY + st));
+          }
+          __syncwarp();
+          n += mine;
+          kv += gives;
+        }
+        uc += mine;
+      }
+      if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN + 2 + t));
+      __syncwarp();
+      if (!tc::mbar_wait(&bars[B_DRAIN + 2 + t], 0, 100000000LL)) *abort_flag = 1;
+    } else if (warp == kClear && P.act) {
+      // ---------------------------------------------------------- masked rows of V
+      uint32_t g = 0;  // V tiles loaded (ring items 2 g + 1)
+      bool ok = true;
+      for (Units U(P); U.left > 0 && ok; U.next(P)) {
+        if (!U.loads(P)) continue;
+#pragma unroll 1
+        for (int j = U.j0; j < U.j1; ++j, ++g) {
+          uint32_t w[KW];
+          state_words(U.bits, P.l, (int64_t)U.tile(j) * KT, w);
+          const uint32_t kv = 2 * g + 1;
+          const int st = kv % NS;
+          ok = ab.all(sb + 8 * (B_FULL + st), (kv / NS));
+          if (!ok) break;
+          if (!all_states(w)) {
+            uint8_t* vt = smem + S::kRing + st * S::KB;
+#pragma unroll
+            for (int i = 0; i < KW; ++i)
+              if (!((w[i] >> lane) & 1u))
+#pragma unroll 1
+                for (int pc = 0; pc < D / 8; ++pc)
+                  *reinterpret_cast<uint4*>(vt + Ly::piece(KT, 32 * i + lane, pc)) =
+                      make_uint4(0u, 0u, 0u, 0u);
+            tc::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) arrive32(sb + 8 * (B_READY + g % kReady));
+        }
+      }
     }
-  } else if (warp < 11) {
-    // ------------------------------------------------------------ MMA issuer of tile t
-    const int t = warp - 9;
-    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-    const uint32_t ts = tb + 128u * t, to = tb + 256u + 128u * t;
-    const uint32_t id_s = tc::idesc_bf16_f32(128, 128, false, false);
-    const uint32_t id_o = tc::idesc_bf16_f32(128, D, false, true);
-    const uint64_t qd0 = Ly::kdesc(tc::smem_u32(smem + S::kQ + t * S::TB));
-    const uint64_t kd0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
-    const uint64_t vd0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), kTile);
-    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, ab.wait(bar, parity, false));
-    };
-    const bool masked = P.act != nullptr;
-    uint32_t kv = 0, gc = 0, uc = 0;
-    bool ok = true;
-    for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
-      const Unit U(P, u);
-      if (U.j0 == U.j1) continue;
-      if (t == 1 && !U.two) {
-        // no rows: give the state tiles back as they come
-        for (int j = 0; j < 2 * (U.j1 - U.j0) && ok; ++j, ++kv) {
-          ok = wwait(&bars[B_FULL + kv % NS], (kv / NS) & 1);
-          if (ok && lane == 0) tc::mbar_arrive(&bars[B_EMPTY + kv % NS]);
-        }
-        continue;
-      }
-      const int buf = uc & 1;
-      if (!wwait(&bars[B_QFULL + 2 * buf + t], (uc >> 1) & 1)) break;
-      ++uc;
-      for (int j = U.j0; j < U.j1; ++j, ++gc) {
-        int st = kv % NS;
-        if (!wwait(&bars[B_FULL + st], (kv / NS) & 1)) { ok = false; break; }
-        // S holds the previous tile's P until its product has completed
-        if (gc >= 1 && !wwait(&bars[B_DONE + t], (gc - 1) & 1)) { ok = false; break; }
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
-          const uint64_t qd = qd0 + (uint64_t)((2 * buf * S::TB) >> 4);
-          const uint64_t kd = kd0 + (uint64_t)((st * S::TB) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < Ly::kSteps; ++ks)
-            tc::mma_ss(ts, qd + Ly::koff(kTile, ks), kd + Ly::koff(kTile, ks), id_s, ks > 0);
-          tc::tc_commit(&bars[B_SFULL + t]);
-          tc::tc_commit(&bars[B_EMPTY + st]);
-        }
-        __syncwarp();
-        ++kv;
-        st = kv % NS;
-        if (!(masked ? wwait(&bars[B_READY + (kv >> 1) % kReady], ((kv >> 1) / kReady) & 1)
-                     : wwait(&bars[B_FULL + st], (kv / NS) & 1))) {
-          ok = false;
-          break;
-        }
-        if (!wwait(&bars[B_PFULL + t], gc & 1)) { ok = false; break; }
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
-          const uint64_t vd = vd0 + (uint64_t)((st * S::TB) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            tc::mma_ts(to, ts + ks * 8, vd + Ly::moff(ks), id_o, (j > U.j0 || ks > 0) ? 1u : 0u);
-          tc::tc_commit(&bars[B_DONE + t]);
-          tc::tc_commit(&bars[B_EMPTY + st]);
-        }
-        __syncwarp();
-        ++kv;
-      }
-    }
-    if (tc::elect_one()) tc::tc_commit(&bars[B_DRAIN + t]);
-    __syncwarp();
-    if (!tc::mbar_wait(&bars[B_DRAIN + t], 0, 100000000LL))
-      set_status(P.status, PACK3D_ERR_TIMEOUT);
-  } else if (P.act) {
-    // ------------------------------------------------------------ masked rows of V
-    uint32_t g = 0;  // V tiles (ring items 2 g + 1)
-    bool ok = true;
-    for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
-      const Unit U(P, u);
-      for (int j = U.j0; j < U.j1; ++j, ++g) {
-        const uint4 b4 = U.bits[U.tile(j)];
-        const uint32_t w[4] = {b4.x, b4.y, b4.z, b4.w};
-        const uint32_t kv = 2 * g + 1;
-        const int st = kv % NS;
-        ok = __all_sync(0xffffffffu, ab.wait(&bars[B_FULL + st], (kv / NS) & 1));
-        if (!ok) break;
-        if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
-          uint8_t* vt = smem + S::kRing + st * S::TB;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!((w[i] >> lane) & 1u))
-#pragma unroll
-              for (int pc = 0; pc < D / 8; ++pc)
-                *reinterpret_cast<uint4*>(vt + Ly::piece(kTile, 32 * i + lane, pc)) =
-                    make_uint4(0u, 0u, 0u, 0u);
-          tc::fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars[B_READY + g % kReady]);
-      }
-    }
-   }
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (tid == 0 && *abort_flag) set_status(P.status, PACK3D_ERR_TIMEOUT);
+  if (warp == kMma) {
     __syncwarp();
     tc::tc_fence_after();
     tc::tmem_dealloc(tbase, 512);
@@ -454,84 +618,93 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
 }
 
 // Joins the splits of each row: lse = log sum_s exp(lse_s), o = sum_s exp(lse_s - lse) o_s, in
-// split order. A group of 16 threads per row.
+// split order. A warp per row, four columns per lane; the weights first, so that the loop over the
+// splits is independent loads.
+constexpr int kMaxSplits = 160;
 template <int D>
 __global__ void __launch_bounds__(128)
     k_cross_join(const float* __restrict__ part_o, const float* __restrict__ part_lse, int nsplit,
                  int64_t rows, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
-  const int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 4);
-  const int t = threadIdx.x & 15;
+  __shared__ float wgt[4][kMaxSplits];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x * 4ll + warp;
   if (row >= rows) return;
   float top = -INFINITY;
-  for (int s = 0; s < nsplit; ++s) top = fmaxf(top, part_lse[s * rows + row]);
+  for (int s = lane; s < nsplit; s += 32) {
+    const float x = part_lse[s * rows + row];
+    wgt[warp][s] = x;
+    top = fmaxf(top, x);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   const float base = top == -INFINITY ? 0.f : top;
-  constexpr int NP = (D / 4 + 15) / 16;
-  float4 a[NP];
-#pragma unroll
-  for (int i = 0; i < NP; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  for (int s = 0; s < nsplit; ++s) {
-    const float ls = part_lse[s * rows + row];
-    if (ls == -INFINITY) continue;  // nothing in this range: its rows were not written
-    const float f = exp2f((ls - base) * kLog2e);
+  for (int s = lane; s < nsplit; s += 32) {
+    const float f = exp2f((wgt[warp][s] - base) * kLog2e);
+    wgt[warp][s] = f;
     sum += f;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int c = (i * 16 + t) * 4;
-      if (c < D) {
-        const float4 x = *reinterpret_cast<const float4*>(part_o + (s * rows + row) * D + c);
-        a[i].x = fmaf(f, x.x, a[i].x);
-        a[i].y = fmaf(f, x.y, a[i].y);
-        a[i].z = fmaf(f, x.z, a[i].z);
-        a[i].w = fmaf(f, x.w, a[i].w);
-      }
-    }
   }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  __syncwarp();
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int c = (i * 16 + t) * 4;
-    if (c < D)
-      *reinterpret_cast<uint2*>(o + row * D + c) =
-          make_uint2(tc::pack_bf16(a[i].x * inv, a[i].y * inv),
-                     tc::pack_bf16(a[i].z * inv, a[i].w * inv));
+  if (lane < D / 4) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < nsplit; ++s) {
+      const float f = wgt[warp][s];
+      // a split without any state has written no row
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (f != 0.f) x = *reinterpret_cast<const float4*>(part_o + (s * rows + row) * D + 4 * lane);
+      a.x = fmaf(f, x.x, a.x);
+      a.y = fmaf(f, x.y, a.y);
+      a.z = fmaf(f, x.z, a.z);
+      a.w = fmaf(f, x.w, a.w);
+    }
+    *reinterpret_cast<uint2*>(o + row * D + 4 * lane) = make_uint2(
+        tc::pack_bf16(a.x * inv, a.y * inv), tc::pack_bf16(a.z * inv, a.w * inv));
   }
-  if (lse && t == 0) lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
+  if (lse && lane == 0) lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
 }
 
 // One block per batch entry: the bits and the list of tiles with an unmasked state.
 __global__ void __launch_bounds__(512)
-    k_cross_mask(const uint8_t* __restrict__ mask, int64_t l, int tiles, int32_t* __restrict__ act,
-                 uint4* __restrict__ bits) {
-  __shared__ uint8_t some[512];
+    k_cross_mask(const uint8_t* __restrict__ mask, int64_t l, int tiles, int tw, int64_t words,
+                 int32_t* __restrict__ act, uint32_t* __restrict__ bits) {
+  __shared__ uint32_t sw[512 * 4 + 16];
   __shared__ int32_t warp_n[16];
   const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint8_t* m = mask + b * l;
   int32_t* list = act + (int64_t)b * (tiles + 1);
+  uint32_t* out = bits + b * words;
   int total = 0;
-  // 512 tiles a round; a warp forms the words of four tiles at a time (16 loads in flight)
+  // 512 tiles a round (every word of the run, the last round's zero padding included); a warp
+  // forms 16 words at a time, their loads in flight together
   for (int base = 0; base < tiles; base += 512) {
-    const int end = min(512, tiles - base);
-    for (int i = warp * 4; i < end; i += 64) {
+    const int64_t w0 = (int64_t)base * tw;
+    const int nw = (int)(base + 512 < tiles ? 512 * tw : words - w0);
+    for (int i = warp * 16; i < nw; i += 256) {
       bool on[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const int64_t at = (int64_t)(base + i) * kTile + 32 * k + lane;
+        const int64_t at = (w0 + i + k) * 32 + lane;
         on[k] = at < l && m[at] != 0;
       }
-      uint32_t w[16];
+      uint32_t mine = 0u;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) w[k] = __ballot_sync(0xffffffffu, on[k]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (lane == k && i + k < end) {
-          bits[(int64_t)b * tiles + base + i + k] =
-              make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-          some[i + k] = (w[4 * k] | w[4 * k + 1] | w[4 * k + 2] | w[4 * k + 3]) != 0u;
-        }
+      for (int k = 0; k < 16; ++k) {
+        const uint32_t w = __ballot_sync(0xffffffffu, on[k]);
+        if (lane == k) mine = w;
+      }
+      if (lane < 16 && i + lane < nw) {
+        out[w0 + i + lane] = mine;
+        sw[i + lane] = mine;
+      }
     }
     __syncthreads();
-    const bool mine = threadIdx.x < end && some[threadIdx.x];
+    bool mine = false;
+    if (base + (int)threadIdx.x < tiles)
+      for (int k = 0; k < tw; ++k) mine = mine || sw[threadIdx.x * tw + k] != 0u;
     const uint32_t have = __ballot_sync(0xffffffffu, mine);
     if (lane == 0) warp_n[warp] = __popc(have);
     __syncthreads();
@@ -548,7 +721,7 @@ __global__ void __launch_bounds__(512)
 
 cudaError_t build_mask(const Problem& p, const MaskTables& m) {
   if (!m.act) return cudaSuccess;
-  k_cross_mask<<<p.batch, 512, 0, p.s>>>(p.mask, p.l, (int)p.tiles(), m.act, m.bits);
+  k_cross_mask<<<p.batch, 512, 0, p.s>>>(p.mask, p.l, m.tiles, m.tw, m.words, m.act, m.bits);
   count_launch();
   return cudaGetLastError();
 }
@@ -556,9 +729,10 @@ cudaError_t build_mask(const Problem& p, const MaskTables& m) {
 // State ranges per unit: only when the units leave SMs idle, at least two tiles each.
 static int fwd_splits(const Problem& p) {
   const int64_t units = p.bh * ((p.np + 2 * kTile - 1) / (2 * kTile));
-  const int64_t tiles = p.tiles();
+  const int64_t tiles = (p.l + fwd_tile(p.d) - 1) / fwd_tile(p.d);
   const int64_t room = sm_count() / (units > 0 ? units : 1);
   int64_t n = tiles / 2 < room ? tiles / 2 : room;
+  if (n > kMaxSplits) n = kMaxSplits;
   return n < 1 ? 1 : (int)n;
 }
 
@@ -575,9 +749,15 @@ static cudaError_t launch_fwd(const Problem& p, const MaskTables& m, void* o, fl
   static std::atomic<uint64_t> attr{0};
   cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(k_cross_fwd<D>), S::kBytes, attr);
   if (e != cudaSuccess) return e;
+  // a split of more registers than the block was launched with would wait for ever
+  static const bool split_fits = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, k_cross_fwd<D>) == cudaSuccess && a.numRegs >= xf::kRegs;
+  }();
+  if (!split_fits) return cudaErrorLaunchOutOfResources;
   CUtensorMap mq, mk, mv, mo;
-  if (!encode_rows<D>(&mq, p.q, p.np, p.bh, kTile) || !encode_rows<D>(&mk, p.k, p.l, p.bh, kTile) ||
-      !encode_rows<D>(&mv, p.v, p.l, p.bh, kTile) || !encode_rows<D>(&mo, o, p.np, p.bh, kTile))
+  if (!encode_rows<D>(&mq, p.q, p.np, p.bh, kTile) || !encode_rows<D>(&mk, p.k, p.l, p.bh, S::KT) ||
+      !encode_rows<D>(&mv, p.v, p.l, p.bh, S::KT) || !encode_rows<D>(&mo, o, p.np, p.bh, kTile))
     return cudaErrorInvalidValue;
   xf::Params P{};
   P.lse = lse;
@@ -590,24 +770,31 @@ static cudaError_t launch_fwd(const Problem& p, const MaskTables& m, void* o, fl
   P.l = p.l;
   P.bh = p.bh;
   P.pairs = (int)((p.np + 2 * kTile - 1) / (2 * kTile));
-  P.tiles = (int)p.tiles();
+  P.words = m.words;
+  P.tiles = m.tiles;
   P.kv_heads = p.kv_heads;
   P.nsplit = fwd_splits(p);
+  P.resident = P.tiles == 1;
   P.scale_log2 = p.scale * kLog2e;
-  P.units = p.bh * P.pairs * P.nsplit;
+  const int64_t units = p.bh * P.pairs * P.nsplit;
+  if (units > INT32_MAX / 2) return cudaErrorInvalidValue;  // more than the memory holds
+  P.units = (int)units;
   if (P.nsplit > 1) {
     P.part_o = static_cast<float*>(ws);
     P.part_lse = reinterpret_cast<float*>(
         static_cast<uint8_t*>(ws) +
         align256((size_t)P.nsplit * p.bh * p.np * D * sizeof(float)));
   }
-  const int64_t cap = sm_count();
-  k_cross_fwd<D><<<(unsigned)(P.units < cap ? P.units : cap), xf::kThreads, S::kBytes, p.s>>>(
+  const int grid = P.units < sm_count() ? P.units : sm_count();
+  const int step = P.resident ? 1 : grid;
+  P.step_pr = step % P.pairs;
+  P.step_bh = step / P.pairs;
+  k_cross_fwd<D><<<grid, xf::kThreads, S::kBytes, p.s>>>(
       mq, mk, mv, mo, P);
   count_launch();
   if (P.nsplit > 1) {
     const int64_t rows = p.bh * p.np;
-    k_cross_join<D><<<(unsigned)((rows + 7) / 8), 128, 0, p.s>>>(P.part_o, P.part_lse, P.nsplit,
+    k_cross_join<D><<<(unsigned)((rows + 3) / 4), 128, 0, p.s>>>(P.part_o, P.part_lse, P.nsplit,
                                                                rows, P.o, lse);
     count_launch();
   }

@@ -125,8 +125,8 @@ struct Params {
   float *dk, *dv;         // partial sums [nsplit][bh][l][D]
   float *delta;           // [bh][np]
   const int32_t* act;
-  const uint4* bits;
-  int64_t np, l, bh;
+  const uint32_t* bits;
+  int64_t np, l, bh, words;
   int tiles, kv_heads, nsplit;
   float scale;
 };
@@ -134,28 +134,23 @@ struct Params {
 // Half-tiles (64 states) of the batch entry: number, place and bits of the i-th.
 struct Halves {
   const int32_t* list;
-  const uint4* bits;
+  const uint32_t* bits;
   int n;
   int64_t l;
   __device__ __forceinline__ Halves(const Params& P, int64_t bh) {
     const int64_t b = bh / P.kv_heads;
     list = P.act ? P.act + b * (P.tiles + 1) + 1 : nullptr;
-    bits = P.act ? P.bits + b * P.tiles : nullptr;
+    bits = P.act ? P.bits + b * P.words : nullptr;
     n = 2 * (P.act ? list[-1] : P.tiles);
     l = P.l;
   }
   __device__ __forceinline__ int64_t at(int i, uint32_t& w0, uint32_t& w1) const {
-    const int t = list ? list[i >> 1] : i >> 1, h = i & 1;
-    uint32_t w[4];
-    if (bits) {
-      const uint4 b = bits[t];
-      w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
-    } else {
-      tail_words(l, t, w);
-    }
-    w0 = h ? w[2] : w[0];
-    w1 = h ? w[3] : w[1];
-    return (int64_t)t * kTile + h * kT;
+    const int64_t at = (int64_t)(list ? list[i >> 1] : i >> 1) * kTile + (i & 1) * kT;
+    uint32_t w[2];
+    state_words(bits, l, at, w);
+    w0 = w[0];
+    w1 = w[1];
+    return at;
   }
 };
 
@@ -333,14 +328,9 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_dkv32(const xs::Params P
   const int64_t bh = blockIdx.y;
   const int half = blockIdx.x / P.nsplit, split = blockIdx.x % P.nsplit;
   const int64_t at = (int64_t)half * kT;
-  uint32_t w[4];
-  if (P.act) {
-    const uint4 b = P.bits[bh / P.kv_heads * P.tiles + (half >> 1)];
-    w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
-  } else {
-    tail_words(P.l, half >> 1, w);
-  }
-  const uint32_t w0 = half & 1 ? w[2] : w[0], w1 = half & 1 ? w[3] : w[1];
+  uint32_t w[2];
+  state_words(P.act ? P.bits + bh / P.kv_heads * P.words : nullptr, P.l, at, w);
+  const uint32_t w0 = w[0], w1 = w[1];
   load_tile<D>(sk, P.k + bh * P.l * D, at, P.l, w0, w1);
   load_tile<D>(sv, P.v + bh * P.l * D, at, P.l, w0, w1);
   float ak[4][D / 16], av[4][D / 16];
@@ -408,7 +398,8 @@ static xs::Params simt_params(const Problem& p, const MaskTables& m) {
   P.np = p.np;
   P.l = p.l;
   P.bh = p.bh;
-  P.tiles = (int)p.tiles();
+  P.words = m.words;
+  P.tiles = m.tiles;
   P.kv_heads = p.kv_heads;
   P.nsplit = 1;
   P.scale = p.scale;

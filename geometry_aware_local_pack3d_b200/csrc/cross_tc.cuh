@@ -93,6 +93,86 @@ __device__ __forceinline__ void bulk_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Barrier operations on 32-bit shared addresses (a generic pointer costs several instructions at
+// each use).
+__device__ __forceinline__ void arrive32(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void commit32(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   bar)
+               : "memory");
+}
+
+// Bounded, abortable wait (as tc::Abort) that suspends on the barrier instead of polling it: a
+// polling warp takes issue slots from the warps of its sub-partition that compute. A wait that runs
+// out raises the CTA's abort word, every other wait then gives up, and the kernel records
+// PACK3D_ERR_TIMEOUT once at its end. The wait is inlined at many places and stays short: these
+// kernels have many roles, and code beyond the instruction cache costs them more than waiting.
+struct Waiter {
+  uint32_t flag;   // shared address of the abort word
+  uint32_t hint;   // nanoseconds of one suspension: a millisecond, or less for a small budget
+  uint32_t tries;  // suspensions that use up the budget, of 2,000 cycles or more each
+  __device__ __forceinline__ Waiter(volatile int* f, long long budget)
+      : flag(tc::smem_u32(const_cast<int*>(f))),
+        hint(budget < 1000000 ? (uint32_t)budget : 1000000u),
+        tries(1u + (uint32_t)(budget / 2000 < 100000000 ? budget / 2000 : 100000000)) {}
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase) const {
+    return wait(tc::smem_u32(bar), phase);
+  }
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase) const {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
+        "mov.u32 n, %4;\n\tmov.u32 %0, 1;\n"
+        "WAIT:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE;\n\t"
+        "ld.volatile.shared.u32 f, [%5];\n\t"
+        "setp.ne.u32 q, f, 0;\n\t"
+        "@q bra FAIL;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra WAIT;\n\t"
+        "st.volatile.shared.u32 [%5], 1;\n"
+        "FAIL:\n\t"
+        "mov.u32 %0, 0;\n"
+        "DONE:\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase & 1), "r"(hint), "r"(tries), "r"(flag)
+        : "memory");
+    return ok != 0;
+  }
+  // by a whole warp
+  __device__ __forceinline__ bool all(uint32_t bar, uint32_t phase) const {
+    return __all_sync(0xffffffffu, wait(bar, phase));
+  }
+  __device__ __forceinline__ bool all(uint64_t* bar, uint32_t phase) const {
+    return __all_sync(0xffffffffu, wait(bar, phase));
+  }
+  // A look at a barrier whose answer is used later: barrier operations queue behind the other
+  // warps' exponentials, and a wait that is satisfied still takes a few hundred cycles.
+  __device__ __forceinline__ static uint32_t probe(uint32_t bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase & 1)
+        : "memory");
+    return ok;
+  }
+  // by a whole warp, after a probe of the same phase
+  __device__ __forceinline__ bool all(uint32_t probed, uint32_t bar, uint32_t phase) const {
+    if (__all_sync(0xffffffffu, probed)) return true;
+    return all(bar, phase);
+  }
+  __device__ __forceinline__ static bool ready(uint64_t* bar, uint32_t phase) {
+    return __all_sync(0xffffffffu, tc::mbar_test_wait(bar, phase & 1));
+  }
+};
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
