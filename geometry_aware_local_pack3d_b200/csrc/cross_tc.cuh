@@ -116,25 +116,25 @@ struct Waiter {
   __device__ __forceinline__ Waiter(volatile int* f, long long budget)
       : flag(tc::smem_u32(const_cast<int*>(f))),
         hint(budget < 1000000 ? (uint32_t)budget : 1000000u),
-        tries(1u + (uint32_t)(budget / 2000 < 100000000 ? budget / 2000 : 100000000)) {}
-  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase) const {
-    return wait(tc::smem_u32(bar), phase);
-  }
+        tries((uint32_t)(budget / 2000 < 100000000 ? budget / 2000 : 100000000)) {}
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase) const {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
-        "mov.u32 n, %4;\n\tmov.u32 %0, 1;\n"
+        "mov.u32 n, %4;\n\tmov.u32 %0, 1;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n"
         "WAIT:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "@p bra DONE;\n\t"
         "ld.volatile.shared.u32 f, [%5];\n\t"
         "setp.ne.u32 q, f, 0;\n\t"
         "@q bra FAIL;\n\t"
+        "setp.eq.u32 q, n, 0;\n\t"
+        "@q st.volatile.shared.u32 [%5], 1;\n\t"
+        "@q bra FAIL;\n\t"
         "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra WAIT;\n\t"
-        "st.volatile.shared.u32 [%5], 1;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@!p bra WAIT;\n\t"
+        "bra DONE;\n"
         "FAIL:\n\t"
         "mov.u32 %0, 0;\n"
         "DONE:\n\t}"
@@ -145,9 +145,6 @@ struct Waiter {
   }
   // by a whole warp
   __device__ __forceinline__ bool all(uint32_t bar, uint32_t phase) const {
-    return __all_sync(0xffffffffu, wait(bar, phase));
-  }
-  __device__ __forceinline__ bool all(uint64_t* bar, uint32_t phase) const {
     return __all_sync(0xffffffffu, wait(bar, phase));
   }
   // A look at a barrier whose answer is used later: barrier operations queue behind the other
@@ -167,9 +164,6 @@ struct Waiter {
   __device__ __forceinline__ bool all(uint32_t probed, uint32_t bar, uint32_t phase) const {
     if (__all_sync(0xffffffffu, probed)) return true;
     return all(bar, phase);
-  }
-  __device__ __forceinline__ static bool ready(uint64_t* bar, uint32_t phase) {
-    return __all_sync(0xffffffffu, tc::mbar_test_wait(bar, phase & 1));
   }
 };
 

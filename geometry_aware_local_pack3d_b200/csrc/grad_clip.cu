@@ -37,14 +37,16 @@ struct Tensor {
   int32_t chunk0;    // first chunk of this tensor within the launch
   int32_t dtype;
 };
-struct Launch {
+// (a short list travels in a short block of parameters: copying one takes longer than a small norm)
+constexpr int kShort = 48;
+template <int N> struct Launch {
   int32_t count, chunks, per_block;  // tensors, chunks, chunks per block
   int32_t words;                     // scaling: words of the norm's sum (every launch's blocks)
-  Tensor t[kPerLaunch];
+  Tensor t[N];
 };
 
 // The tensor that holds chunk c (the last one whose first chunk is not after c).
-__device__ __forceinline__ int find(const Launch& L, int c) {
+template <int N> __device__ __forceinline__ int find(const Launch<N>& L, int c) {
   int lo = 0, hi = L.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -102,8 +104,9 @@ __device__ __forceinline__ double block_sum(double s, double* red) {
   return r;
 }
 
+template <int N>
 __global__ void __launch_bounds__(kThreads)
-    k_grad_sq(const __grid_constant__ Launch L, double* __restrict__ words) {
+    k_grad_sq(const __grid_constant__ Launch<N> L, double* __restrict__ words) {
   __shared__ double red[kThreads / 32];
   const int c0 = blockIdx.x * L.per_block, c1 = min(L.chunks, c0 + L.per_block);
   double total = 0.0;
@@ -168,8 +171,9 @@ __device__ __forceinline__ void scale_piece(uint4 v, int dt, float coef, uint4* 
   }
 }
 
+template <int N>
 __global__ void __launch_bounds__(kThreads)
-    k_grad_scale(const __grid_constant__ Launch L, const double* __restrict__ words,
+    k_grad_scale(const __grid_constant__ Launch<N> L, const double* __restrict__ words,
                  float max_norm, float* __restrict__ norm) {
   __shared__ double red[kThreads / 32];
   const float nrm = norm_of(words, L.words, red);
@@ -257,12 +261,13 @@ bool overlapping(const void* const* grads, void* const* outs, const int64_t* cou
 }
 
 // One launch's tensors [i0, i1): as many as fit.
-int fill(Launch* L, const void* const* grads, void* const* outs, const int64_t* counts,
+template <int N>
+int fill(Launch<N>* L, const void* const* grads, void* const* outs, const int64_t* counts,
          const int* dtypes, int n, int i0) {
   int i = i0;
   int64_t chunks = 0;
   L->count = 0;
-  for (; i < n && L->count < kPerLaunch; ++i) {
+  for (; i < n && L->count < N; ++i) {
     if (!counts[i]) continue;
     const int64_t head = reinterpret_cast<uintptr_t>(grads[i]) & 15;
     const int64_t c = (head + counts[i] * elem(dtypes[i]) + kChunkBytes - 1) / kChunkBytes;
@@ -279,7 +284,7 @@ int fill(Launch* L, const void* const* grads, void* const* outs, const int64_t* 
   return i;
 }
 
-int grid_of(Launch* L) {
+template <int N> int grid_of(Launch<N>* L) {
   int cap = kBlocksPerSm * sm_count();
   if (cap > kMaxBlocks) cap = kMaxBlocks;
   const int blocks = L->chunks < cap ? L->chunks : cap;
@@ -294,19 +299,45 @@ size_t workspace_bytes(int n) {
 }
 
 // The sum of squares: returns the words written.
+template <int N>
 int sum_squares(const void* const* grads, const int64_t* counts, const int* dtypes, int n,
                 double* words, cudaStream_t s) {
-  Launch L{};
+  Launch<N> L;
   int used = 0;
   for (int i = 0; i < n;) {
     i = fill(&L, grads, nullptr, counts, dtypes, n, i);
     const int grid = grid_of(&L);
     if (!grid) continue;
-    k_grad_sq<<<grid, kThreads, 0, s>>>(L, words + used);
+    L.words = 0;
+    k_grad_sq<N><<<grid, kThreads, 0, s>>>(L, words + used);
     count_launch();
     used += grid;
   }
   return used;
+}
+
+// The scaling; the norm is written by the first launch, or by none if every tensor is empty.
+template <int N>
+bool scale(const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes,
+           int n, float max_norm, float* norm, const double* words, int used, cudaStream_t s) {
+  Launch<N> L;
+  bool told = false;
+  for (int i = 0; i < n;) {
+    i = fill(&L, grads, outs, counts, dtypes, n, i);
+    const int grid = grid_of(&L);
+    if (!grid) continue;
+    L.words = used;
+    k_grad_scale<N><<<grid, kThreads, 0, s>>>(L, words, max_norm, told ? nullptr : norm);
+    told = true;
+    count_launch();
+  }
+  return told;
+}
+
+int sum_squares_of(const void* const* grads, const int64_t* counts, const int* dtypes, int n,
+                   double* words, cudaStream_t s) {
+  return n <= kShort ? sum_squares<kShort>(grads, counts, dtypes, n, words, s)
+                     : sum_squares<kPerLaunch>(grads, counts, dtypes, n, words, s);
 }
 
 pack3d_status check_workspace(void* workspace, size_t bytes, int n) {
@@ -334,7 +365,7 @@ extern "C" pack3d_status pack3d_grad_norm(const void* const* grads, const int64_
   if ((st = gc::check_workspace(workspace, workspace_bytes, n_tensors)) != PACK3D_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* words = static_cast<double*>(workspace);
-  const int used = gc::sum_squares(grads, counts, dtypes, n_tensors, words, s);
+  const int used = gc::sum_squares_of(grads, counts, dtypes, n_tensors, words, s);
   gc::k_grad_norm<<<1, gc::kThreads, 0, s>>>(words, used, norm);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? PACK3D_OK : PACK3D_ERR_CUDA;
@@ -358,18 +389,12 @@ extern "C" pack3d_status pack3d_clip_grad_norm(const void* const* grads, void* c
   if (gc::overlapping(grads, outs, counts, dtypes, n_tensors)) return PACK3D_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* words = static_cast<double*>(workspace);
-  const int used = gc::sum_squares(grads, counts, dtypes, n_tensors, words, s);
-  gc::Launch L{};
-  bool told = false;
-  for (int i = 0; i < n_tensors;) {
-    i = gc::fill(&L, grads, outs, counts, dtypes, n_tensors, i);
-    const int grid = gc::grid_of(&L);
-    if (!grid) continue;
-    L.words = used;
-    gc::k_grad_scale<<<grid, gc::kThreads, 0, s>>>(L, words, max_norm, told ? nullptr : norm);
-    told = true;
-    count_launch();
-  }
+  const int used = gc::sum_squares_of(grads, counts, dtypes, n_tensors, words, s);
+  const bool told =
+      n_tensors <= gc::kShort
+          ? gc::scale<gc::kShort>(grads, outs, counts, dtypes, n_tensors, max_norm, norm, words, used, s)
+          : gc::scale<gc::kPerLaunch>(grads, outs, counts, dtypes, n_tensors, max_norm, norm, words,
+                                      used, s);
   if (!told) {  // nothing but empty tensors: the norm is zero
     gc::k_grad_norm<<<1, gc::kThreads, 0, s>>>(words, used, norm);
     count_launch();
