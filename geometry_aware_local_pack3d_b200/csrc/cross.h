@@ -66,6 +66,13 @@ cudaError_t build_mask(const Problem& p, const MaskTables& m);
 size_t fwd_tc_bytes(const Problem& p);
 cudaError_t fwd_tc(const Problem& p, const MaskTables& m, void* o, float* lse, void* ws);
 cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse);
+// bf16 forward and backward of a short context (no mask tables)
+bool short_fwd(const Problem& p);
+cudaError_t fwd_short(const Problem& p, void* o, float* lse);
+bool short_bwd(const Problem& p);
+size_t bwd_short_bytes(const Problem& p);
+cudaError_t bwd_short(const Problem& p, const void* o, const float* lse, const void* dO, void* dq,
+                      void* dk, void* dv, void* ws);
 // backward
 size_t bwd_tc_bytes(const Problem& p);
 cudaError_t bwd_tc(const Problem& p, const MaskTables& m, const void* o, const float* lse,

@@ -54,6 +54,7 @@ pack3d_status make(xa::Problem* p, int dtype, int batch, int heads, int kv_heads
 
 size_t bytes_of(const xa::Problem& p, bool mask, bool backward) {
   if (p.l == 0 || p.np == 0) return 0;
+  if (backward ? xa::short_bwd(p) : xa::short_fwd(p)) return backward ? xa::bwd_short_bytes(p) : 0;
   const bool tc = p.dtype == PACK3D_BF16;
   const size_t own = backward ? (tc ? xa::bwd_tc_bytes(p) : xa::bwd_simt_bytes(p))
                               : (tc ? xa::fwd_tc_bytes(p) : 0);
@@ -109,6 +110,7 @@ extern "C" pack3d_status pack3d_cross_attn_fwd(const void* q, const void* k, con
   if (l == 0)
     return cuda_status(empty_rows(o, rows * p.d * (dtype == PACK3D_BF16 ? 2 : 4), lse, rows, p.s));
   if ((st = check_workspace(p, workspace, workspace_bytes, false)) != PACK3D_OK) return st;
+  if (xa::short_fwd(p)) return cuda_status(xa::fwd_short(p, o, lse));
   const int tw = xa::mask_tile_words(p, false);
   const xa::MaskTables m = xa::mask_at(p, tw, workspace);
   cudaError_t e = xa::build_mask(p, m);
@@ -154,6 +156,7 @@ extern "C" pack3d_status pack3d_cross_attn_bwd(const void* q, const void* k, con
     return cuda_status(e);
   }
   if ((st = check_workspace(p, workspace, workspace_bytes, true)) != PACK3D_OK) return st;
+  if (xa::short_bwd(p)) return cuda_status(xa::bwd_short(p, o, lse, dO, dq, dk, dv, workspace));
   const int tw = xa::mask_tile_words(p, true);
   const xa::MaskTables m = xa::mask_at(p, tw, workspace);
   cudaError_t e = xa::build_mask(p, m);

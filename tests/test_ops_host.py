@@ -14,7 +14,7 @@ FAKE, ODD = 0x100000, 0x100004
 
 
 def cross_fwd(**kw):
-    a = dict(q=FAKE, k=FAKE, v=FAKE, mask=None, dtype=1, batch=1, heads=2, kv_heads=2, n=10, l=10, d=96,
+    a = dict(q=FAKE, k=FAKE, v=FAKE, mask=None, dtype=1, batch=1, heads=2, kv_heads=2, n=10, l=200, d=96,
              scale=0.1, o=FAKE, lse=None, ws=None, bytes=0, status=None)
     a.update(kw)
     return b.lib().pack3d_cross_attn_fwd(a["q"], a["k"], a["v"], a["mask"], a["dtype"], a["batch"],
@@ -58,10 +58,11 @@ def test_cross_workspace_sizes():
     f = b.pack3d_cross_attn_workspace_bytes
     assert f(1, 1, 2, 2, 10, 10, 50) == 0 and f(1, 1, 3, 2, 10, 10, 96) == 0
     assert f(1, 1, 2, 2, 0, 10, 96, True, True) == 0 and f(1, 1, 2, 2, 10, 0, 96, True, True) == 0
-    assert f(1, 1, 2, 2, 300, 77, 96) == 0
-    assert f(1, 1, 2, 2, 300, 77, 96, True) > 0
+    assert f(1, 1, 2, 2, 300, 77, 96) == 0 and f(1, 1, 2, 2, 300, 77, 96, True) == 0  # short contexts
+    assert f(1, 200, 2, 2, 300, 300, 96) == 0 and f(1, 200, 2, 2, 300, 300, 96, True) > 0
     assert f(1, 1, 2, 2, 1, 8192, 96) > 0                       # the states are split
-    assert f(1, 1, 2, 2, 300, 77, 96, False, True) >= 2 * 384 * 8
+    assert f(1, 1, 2, 2, 300, 300, 96, False, True) >= 2 * 384 * 8
+    assert f(1, 1, 2, 2, 300, 77, 96, False, True) > 0
     # the sizes do not wrap: a long context's partial sums
     assert f(0, 1, 8, 8, 1 << 20, 1 << 20, 128, False, True) >= 8 * (1 << 20) * 4
 
