@@ -3,9 +3,8 @@
 //   p_ij = exp(tau <q_i, k_j> - lse_i),  D_i = <dO_i, o_i>,  dS_ij = p_ij (<dO_i, v_j> - D_i) tau,
 //   dq_i = sum_j dS_ij k_j,   dk_j = sum_i dS_ij q_i,   dv_j = sum_i p_ij dO_i.
 //
-//   k_cross_rows  per row (-lse log2(e), D tau), padded to whole tiles of rows
-//   k_cross_dq    row-major: a CTA walks 128-row tiles; per 64 states S = q K^T and dP = dO V^T,
-//                 dS in bf16 over S, dq += dS K. Two CTAs per SM, so that one tile's products run
+//   k_cross_dq    row-major: a CTA walks 128-row tiles; first D of the tile's rows (left for
+//                 k_cross_dkv too); per 64 states S = q K^T and dP = dO V^T, dS in bf16, dq += dS K. Two CTAs per SM, so that one tile's products run
 //                 under the other's elementwise pass and epilogue.
 //   k_cross_dkv   state-major: a CTA owns 128 states of one problem and a range of rows; per 64 rows
 //                 S^T = K q^T and dP^T = V dO^T (double-buffered in TMEM), P^T and dS^T in bf16 over
@@ -41,7 +40,9 @@ __device__ __forceinline__ float2 f2(uint32_t a, uint32_t b) {
 }
 
 struct Params {
-  const float2* rows;  // [bh][npad]
+  float2* rows;  // [bh][npad] (-lse log2(e), D tau): written by k_cross_dq, read by k_cross_dkv
+  const __nv_bfloat16* o;
+  const float* lse;
   const int32_t* act;
   const uint32_t* bits;
   int32_t* status;
@@ -53,36 +54,6 @@ struct Params {
   float *part_k, *part_v;   // [nsplit][bh][l][D] otherwise
 };
 }  // namespace xb
-
-// ------------------------------------------------------------------------------- row data
-template <int D>
-__global__ void __launch_bounds__(256)
-    k_cross_rows(const __nv_bfloat16* __restrict__ dO, const __nv_bfloat16* __restrict__ o,
-                 const float* __restrict__ lse, int64_t np, int64_t npad, int64_t bh, float scale,
-                 float2* __restrict__ rows) {
-  constexpr int G = D <= 64 ? 8 : 16;  // threads per row, a 16-byte piece each
-  const int64_t i = blockIdx.x * (int64_t)(256 / G) + threadIdx.x / G;
-  const int t = threadIdx.x % G;
-  if (i >= bh * npad) return;  // whole groups: the shuffles below stay inside one
-  const int64_t p = i / npad, r = i % npad;
-  const int64_t row = p * np + r;
-  float s = 0.f;
-  if (r < np && t < D / 8) {
-    float a[8], b[8];
-    Vec<__nv_bfloat16>::load(dO + row * D + t * 8, a);
-    Vec<__nv_bfloat16>::load(o + row * D + t * 8, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
-  }
-  const uint32_t grp = (G == 16 ? 0xffffu : 0xffu) << (threadIdx.x & 31 & ~(G - 1));
-#pragma unroll
-  for (int x = G / 2; x > 0; x >>= 1) s += __shfl_xor_sync(grp, s, x);
-  if (t == 0) {
-    const float le = r < np ? lse[row] : -INFINITY;
-    // a row without any state, and the padding: P = 0
-    rows[i] = make_float2(le == -INFINITY ? -INFINITY : -le * kLog2e, s * scale);
-  }
-}
 
 // -------------------------------------------------------------------------------------- dq
 namespace xq {
@@ -100,11 +71,18 @@ template <int D> struct Smem {
 constexpr int kMaxSlots = 6, kReady = 8;
 enum {
   B_QFULL = 0, B_QEMPTY = 1, B_FULL = 2, B_EMPTY = B_FULL + kMaxSlots,
-  B_READY = B_EMPTY + kMaxSlots, B_SFULL = B_READY + kReady, B_PFULL, B_DONE, B_STAGED, B_DRAIN,
-  B_COUNT
+  B_READY = B_EMPTY + kMaxSlots, B_SFULL = B_READY + kReady, B_SFREE, B_PFULL, B_DONE, B_STAGED,
+  B_DRAIN, B_COUNT
 };
 static_assert(8 * B_COUNT + 16 <= 512, "barrier area");
-constexpr uint32_t kS = 0, kP = 64, kO = 128;  // TMEM columns: S (then dS), dP, dq
+// TMEM columns of 256: S, dP, dS (bf16), dq. Where dS has columns of its own (d <= 96), the next
+// step's S and dP are formed as soon as this step's have been read; at d = 128 dS lies over S and
+// they wait for this step's last product.
+template <int D> struct Cols {
+  static constexpr bool kOwn = D <= 96;
+  static constexpr uint32_t kS = 0, kP = 64, kD = kOwn ? 128 : 0, kO = kOwn ? 160 : 128;
+  static_assert(kO + D <= 256, "tensor memory");
+};
 
 // A unit's problem, first row and steps of 64 states (the batch entry's listed tiles, halved).
 struct Unit {
@@ -142,13 +120,15 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
   using namespace xq;
   using S = Smem<D>;
   using Ly = Lay<D>;
+  using C = Cols<D>;
   constexpr int NS = S::kSlots;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kBar + 8 * B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kBar + 8 * B_COUNT + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  tc::Abort ab{abort_flag, P.status, P.budget};
+  const Waiter ab(abort_flag, P.budget);
+  const uint32_t sb = tc::smem_u32(bars);  // barrier i at sb + 8 i
   if (tid == 0) {
     tc::mbar_init(&bars[B_QFULL], 1);
     tc::mbar_init(&bars[B_QEMPTY], 1);
@@ -158,6 +138,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
     }
     for (int i = 0; i < kReady; ++i) tc::mbar_init(&bars[B_READY + i], 1);
     tc::mbar_init(&bars[B_SFULL], 1);
+    tc::mbar_init(&bars[B_SFREE], 128);
     tc::mbar_init(&bars[B_PFULL], 128);
     tc::mbar_init(&bars[B_DONE], 1);
     tc::mbar_init(&bars[B_STAGED], 128);
@@ -175,25 +156,62 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
     // ------------------------------------------------------------ elementwise and epilogue
     const int rin = warp * 32 + lane;
     const uint32_t tl = tbase + ((uint32_t)(warp * 32) << 16);
-    uint32_t gc = 0, staged = 0;
+    uint32_t gc = 0, uc = 0, staged = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
       const Unit U(P, u);
-      const float2 rd = P.rows[U.bh * P.npad + U.row0 + rin];
+      // the row's D = <dO, o> and lse, for this kernel and for k_cross_dkv; a row without any state,
+      // and the padding, get P = 0
+      float2 rd = make_float2(-INFINITY, 0.f);
+      {
+        const int64_t row = U.row0 + rin, at = U.bh * P.np + row;
+        uint4 o[D / 8];
+        const bool in = row < P.np && U.n;
+        float le = -INFINITY, d = 0.f;
+        if (in) {
+          le = P.lse[at];
+#pragma unroll
+          for (int pc = 0; pc < D / 8; ++pc)
+            o[pc] = *reinterpret_cast<const uint4*>(P.o + at * D + pc * 8);
+        }
+        if (U.n) ok = ab.all(sb + 8 * (B_QFULL), uc++);
+        if (!ok) break;
+        if (in) {
+#pragma unroll
+          for (int pc = 0; pc < D / 8; ++pc) {
+            float a[8], b[8];
+            Vec<__nv_bfloat16>::unpack(o[pc], a);
+            Vec<__nv_bfloat16>::load_shared(
+                reinterpret_cast<const __nv_bfloat16*>(smem + S::kG + Ly::piece(kTile, rin, pc)), b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d = fmaf(a[e], b[e], d);
+          }
+          if (le != -INFINITY) rd = make_float2(-le * kLog2e, d * P.scale);
+        }
+        P.rows[U.bh * P.npad + row] = rd;
+      }
       const float2 nl2 = make_float2(rd.x, rd.x), nd2 = make_float2(-rd.y, -rd.y);
       const float2 sl2 = make_float2(P.scale_log2, P.scale_log2);
       const float2 sc2 = make_float2(P.scale, P.scale);
+      uint32_t seen = 0;
+#pragma unroll 1
       for (int j = 0; j < U.n; ++j, ++gc) {
         uint32_t w[2];
         U.words(P.l, j, w);
-        if (!__all_sync(0xffffffffu, ab.wait(&bars[B_SFULL], gc & 1))) { ok = false; break; }
+        ok = ab.all(seen, sb + 8 * (B_SFULL), gc);
+        if (!ok) break;
         tc::tc_fence_after();
+        const uint32_t done = ab.probe(sb + 8 * (B_DONE), gc - 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t sv[32], dv[32], pk[16];
-          tc::tmem_ld32(tl + kS + 32 * h, sv);
-          tc::tmem_ld32(tl + kP + 32 * h, dv);
+          tc::tmem_ld32(tl + C::kS + 32 * h, sv);
+          tc::tmem_ld32(tl + C::kP + 32 * h, dv);
           tc::tmem_wait_ld();
+          if (C::kOwn && h == 1) {
+            tc::tc_fence_before();
+            arrive32(sb + 8 * (B_SFREE));
+          }
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
             const float2 x = tc::fma2(xb::f2(sv[k], sv[k + 1]), sl2, nl2);
@@ -205,15 +223,23 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
             }
             pk[k >> 1] = tc::pack_bf16(ds.x, ds.y);
           }
-          // over S columns that this thread has read
-          tc::tmem_st16(tl + kS + 16 * h, pk);
+          if (C::kOwn && h == 0 && gc) {
+            // dS is the previous step's until its product has completed
+            ok = ab.all(done, sb + 8 * (B_DONE), gc - 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+          }
+          // (over S: columns that this thread has read)
+          tc::tmem_st16(tl + C::kD + 16 * h, pk);
         }
+        if (!ok) break;
+        if (C::kOwn) seen = ab.probe(sb + 8 * (B_SFULL), gc + 1);
         tc::tmem_wait_st();
         tc::tc_fence_before();
-        tc::mbar_arrive(&bars[B_PFULL]);
+        arrive32(sb + 8 * (B_PFULL));
       }
       if (!ok) break;
-      if (U.n && !__all_sync(0xffffffffu, ab.wait(&bars[B_DONE], (gc - 1) & 1))) break;
+      if (U.n && !ab.all(sb + 8 * (B_DONE), (gc - 1) & 1)) break;
       if (!U.n) {
         // no state: zero rows
         if (U.row0 + rin < P.np) {
@@ -228,7 +254,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
 #pragma unroll
       for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
-        tc::tmem_ld16(tl + kO + c, o);
+        tc::tmem_ld16(tl + C::kO + c, o);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -244,15 +270,15 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
       }
       tc::tc_fence_before();
       tc::fence_proxy_async_smem();
-      tc::mbar_arrive(&bars[B_STAGED]);
+      arrive32(sb + 8 * (B_STAGED));
       if (rin == 0) {
-        if (!ab.wait(&bars[B_STAGED], staged++ & 1)) ok = false;
+        if (!ab.wait(sb + 8 * (B_STAGED), staged++ & 1)) ok = false;
 #pragma unroll
         for (int c = 0; c < Ly::NB && ok; ++c)
           tma_store_3d(&mo, smem + S::kQ + c * kTile * Ly::RB, c * Ly::CW, (int)U.row0, (int)U.bh);
         bulk_commit();
         bulk_wait_read();
-        tc::mbar_arrive(&bars[B_QEMPTY]);
+        arrive32(sb + 8 * (B_QEMPTY));
       }
       ok = __all_sync(0xffffffffu, ok);  // a warp leaves the loop as one
     }
@@ -265,7 +291,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
       for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
         const Unit U(P, u);
         if (!U.n) continue;
-        if (uc && !ab.wait(&bars[B_QEMPTY], (uc - 1) & 1)) break;
+        if (uc && !ab.wait(sb + 8 * (B_QEMPTY), (uc - 1) & 1)) break;
         tc::mbar_expect_tx(&bars[B_QFULL], 2 * S::TB);
         load_rows<D>(smem + S::kQ, &mq, kTile, U.row0, (int)U.bh, &bars[B_QFULL]);
         load_rows<D>(smem + S::kG, &mg, kTile, U.row0, (int)U.bh, &bars[B_QFULL]);
@@ -274,7 +300,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
           const int64_t at = U.at(j);
           for (int x = 0; x < 2; ++x, ++kv) {
             const int st = kv % NS;
-            if (kv >= (uint32_t)NS && !ab.wait(&bars[B_EMPTY + st], ((kv / NS) - 1) & 1)) {
+            if (kv >= (uint32_t)NS && !ab.wait(sb + 8 * (B_EMPTY + st), ((kv / NS) - 1) & 1)) {
               ok = false;
               break;
             }
@@ -297,55 +323,64 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
     const uint64_t gd = Ly::kdesc(tc::smem_u32(smem + S::kG));
     const uint64_t kd0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
     const uint64_t km0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
-    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, ab.wait(bar, parity, false));
-    };
     const bool masked = P.act != nullptr;
-    uint32_t kv = 0, gc = 0, uc = 0;
+    uint32_t gc = 0, uc = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
       const Unit U(P, u);
       if (!U.n) continue;
-      if (!wwait(&bars[B_QFULL], uc & 1)) break;
+      if (!ab.all(sb + 8 * (B_QFULL), uc & 1)) break;
       ++uc;
-      for (int j = 0; j < U.n; ++j, ++gc, kv += 2) {
-        const int sv = kv % NS, sk = (kv + 1) % NS;
-        ok = masked ? wwait(&bars[B_READY + gc % kReady], (gc / kReady) & 1)
-                    : wwait(&bars[B_FULL + sk], ((kv + 1) / NS) & 1);
-        ok = ok && wwait(&bars[B_FULL + sv], (kv / NS) & 1);
-        // S and dP hold the previous step's dS until its product has completed
-        if (ok && gc >= 1) ok = wwait(&bars[B_DONE], (gc - 1) & 1);
+      // step i: S and dP of step i, then (one step later where dS has columns of its own) dq += dS K
+      constexpr int kLag = C::kOwn ? 1 : 0;
+#pragma unroll 1
+      for (int i = 0; i < U.n + kLag && ok; ++i) {
+        if (i < U.n) {
+          const uint32_t kv = 2 * (gc + i), g = gc + i;  // V and K of the step
+          const int sv = kv % NS, sk = (kv + 1) % NS;
+          ok = masked ? ab.all(sb + 8 * (B_READY + g % kReady), g / kReady)
+                      : ab.all(sb + 8 * (B_FULL + sk), (kv + 1) / NS);
+          ok = ok && ab.all(sb + 8 * (B_FULL + sv), kv / NS);
+          // S and dP have been read (and with dS over S: its product has completed)
+          if (g >= 1) ok = ok && ab.all(sb + 8 * (C::kOwn ? B_SFREE : B_DONE), g - 1);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint64_t ko = (uint64_t)((sk * S::HB) >> 4), vo = (uint64_t)((sv * S::HB) >> 4);
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < Ly::kSteps; ++ks) {
+              tc::mma_ss(tb + C::kS, qd + Ly::koff(kTile, ks), kd0 + ko + Ly::koff(xb::kHalf, ks),
+                         id_s, ks > 0);
+              tc::mma_ss(tb + C::kP, gd + Ly::koff(kTile, ks), kd0 + vo + Ly::koff(xb::kHalf, ks),
+                         id_s, ks > 0);
+            }
+            commit32(sb + 8 * (B_SFULL));
+            commit32(sb + 8 * (B_EMPTY + sv));
+          }
+          __syncwarp();
+        }
+        const int j = i - kLag;
+        if (j < 0) continue;
+        const int sk = (2 * (gc + j) + 1) % NS;
+        ok = ab.all(sb + 8 * (B_PFULL), gc + j);
         if (!ok) break;
         tc::tc_fence_after();
-        const uint64_t ko = (uint64_t)((sk * S::HB) >> 4), vo = (uint64_t)((sv * S::HB) >> 4);
         if (tc::elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < Ly::kSteps; ++ks) {
-            tc::mma_ss(tb + kS, qd + Ly::koff(kTile, ks), kd0 + ko + Ly::koff(xb::kHalf, ks), id_s,
-                       ks > 0);
-            tc::mma_ss(tb + kP, gd + Ly::koff(kTile, ks), kd0 + vo + Ly::koff(xb::kHalf, ks), id_s,
-                       ks > 0);
-          }
-          tc::tc_commit(&bars[B_SFULL]);
-          tc::tc_commit(&bars[B_EMPTY + sv]);
-        }
-        __syncwarp();
-        if (!wwait(&bars[B_PFULL], gc & 1)) { ok = false; break; }
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
+          const uint64_t ko = (uint64_t)((sk * S::HB) >> 4);
 #pragma unroll
           for (int ks = 0; ks < xb::kHalf / 16; ++ks)
-            tc::mma_ts(tb + kO, tb + kS + ks * 8, km0 + ko + Ly::moff(ks), id_o,
+            tc::mma_ts(tb + C::kO, tb + C::kD + ks * 8, km0 + ko + Ly::moff(ks), id_o,
                        (j > 0 || ks > 0) ? 1u : 0u);
-          tc::tc_commit(&bars[B_DONE]);
-          tc::tc_commit(&bars[B_EMPTY + sk]);
+          commit32(sb + 8 * (B_DONE));
+          commit32(sb + 8 * (B_EMPTY + sk));
         }
         __syncwarp();
       }
+      gc += U.n;
     }
-    if (tc::elect_one()) tc::tc_commit(&bars[B_DRAIN]);
+    if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN));
     __syncwarp();
-    if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) set_status(P.status, PACK3D_ERR_TIMEOUT);
+    if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) *abort_flag = 1;
   } else if (warp == 6 && P.act) {
     // ------------------------------------------------------------ masked rows of K
     uint32_t g = 0;
@@ -357,7 +392,9 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
         U.words(P.l, j, w);
         const uint32_t kv = 2 * g + 1;
         const int st = kv % NS;
-        ok = __all_sync(0xffffffffu, ab.wait(&bars[B_FULL + st], (kv / NS) & 1));
+        // V first: a slot holds V and K in turn, and every phase of its barrier has to be followed
+        ok = ab.all(sb + 8 * (B_FULL + (kv - 1) % NS), (kv - 1) / NS) &&
+             ab.all(sb + 8 * (B_FULL + st), kv / NS);
         if (!ok) break;
         if ((w[0] & w[1]) != 0xffffffffu) {
           uint8_t* kt = smem + S::kRing + st * S::HB;
@@ -371,12 +408,13 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
           tc::fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars[B_READY + g % kReady]);
+        if (lane == 0) arrive32(sb + 8 * (B_READY + g % kReady));
       }
     }
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort_flag) set_status(P.status, PACK3D_ERR_TIMEOUT);
   if (warp == 5) {
     __syncwarp();
     tc::tc_fence_after();
@@ -421,7 +459,8 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kBar + 8 * B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kBar + 8 * B_COUNT + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  tc::Abort ab{abort_flag, P.status, P.budget};
+  const Waiter ab(abort_flag, P.budget);
+  const uint32_t sb = tc::smem_u32(bars);  // barrier i at sb + 8 i
   const int64_t item = blockIdx.x;
   const int split = (int)(item % P.nsplit);
   const int kt = (int)((item / P.nsplit) % P.tiles);
@@ -462,9 +501,9 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
     const float2 sc2 = make_float2(P.scale, P.scale);
     bool ok = true;
     for (int i = b; i < NT; i += 2) {
-      if (!__all_sync(0xffffffffu, ab.wait(&bars[B_SFULL + b], (i >> 1) & 1))) { ok = false; break; }
+      if (!ab.all(sb + 8 * (B_SFULL + b), (i >> 1) & 1)) { ok = false; break; }
       // the row data came with the step's tiles
-      if (!__all_sync(0xffffffffu, ab.wait(&bars[B_QFULL + i % kStages], (i / kStages) & 1))) {
+      if (!ab.all(sb + 8 * (B_QFULL + i % kStages), (i / kStages) & 1)) {
         ok = false;
         break;
       }
@@ -493,13 +532,13 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
       }
       tc::tmem_wait_st();
       tc::tc_fence_before();
-      tc::mbar_arrive(&bars[B_PFULL + b]);
+      arrive32(sb + 8 * (B_PFULL + b));
     }
     // warps 0-3 write dk, warps 4-7 dv, once every step's products have completed (a barrier of
     // its own: a group has not followed the other group's phases of B_DONE)
     const int64_t row = (int64_t)kt * kTile + rin;
     const bool in = (w[rin >> 5] >> (rin & 31)) & 1u;
-    if (ok && NT > 0) ok = __all_sync(0xffffffffu, ab.wait(&bars[B_ALL], 0));
+    if (ok && NT > 0) ok = ab.all(sb + 8 * (B_ALL), 0);
     tc::tc_fence_after();
     if (ok) {
 #pragma unroll
@@ -542,7 +581,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
       int i = 0;
       for (; i < NT; ++i) {
         const int st = i % kStages;
-        if (i >= kStages && !ab.wait(&bars[B_QEMPTY + st], ((i / kStages) - 1) & 1)) break;
+        if (i >= kStages && !ab.wait(sb + 8 * (B_QEMPTY + st), ((i / kStages) - 1) & 1)) break;
         const int64_t row = (i0 + i) * xb::kHalf;
         tc::mbar_expect_tx(&bars[B_QFULL + st], 2 * S::HB + S::kRowB);
         load_rows<D>(smem + S::kRing + 2 * st * S::HB, &mq, xb::kHalf, row, (int)bh,
@@ -566,14 +605,11 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
     const uint64_t rk0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
     const uint64_t rm0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
     constexpr uint64_t HO = (uint64_t)(S::HB >> 4);
-    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, ab.wait(bar, parity, false));
-    };
     // S^T and dP^T of step i into buffer i % 2, free once step i - 2's products completed
     auto issue_s = [&](int i) -> bool {
       const int st = i % kStages, b = i & 1;
-      if (!wwait(&bars[B_QFULL + st], (i / kStages) & 1)) return false;
-      if (i >= 2 && !wwait(&bars[B_DONE + b], ((i - 2) >> 1) & 1)) return false;
+      if (!ab.all(sb + 8 * (B_QFULL + st), (i / kStages) & 1)) return false;
+      if (i >= 2 && !ab.all(sb + 8 * (B_DONE + b), ((i - 2) >> 1) & 1)) return false;
       tc::tc_fence_after();
       if (tc::elect_one()) {
         const uint64_t qo = rk0 + 2 * st * HO, go = qo + HO;
@@ -584,16 +620,16 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
           tc::mma_ss(tb + p_col(b), vd + Ly::koff(kTile, ks), go + Ly::koff(xb::kHalf, ks), id_s,
                      ks > 0);
         }
-        tc::tc_commit(&bars[B_SFULL + b]);
+        commit32(sb + 8 * (B_SFULL + b));
       }
       __syncwarp();
       return true;
     };
-    bool ok = NT > 0 && wwait(&bars[B_AFULL], 0);
+    bool ok = NT > 0 && ab.all(sb + 8 * (B_AFULL), 0);
     for (int i = 0; i < 2 && i < NT && ok; ++i) ok = issue_s(i);
     for (int i = 0; i < NT && ok; ++i) {
       const int st = i % kStages, b = i & 1;
-      if (!wwait(&bars[B_PFULL + b], (i >> 1) & 1)) break;
+      if (!ab.all(sb + 8 * (B_PFULL + b), (i >> 1) & 1)) break;
       tc::tc_fence_after();
       if (tc::elect_one()) {
         const uint64_t qm = rm0 + 2 * st * HO, gm = qm + HO;
@@ -604,19 +640,20 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
           tc::mma_ts(tb + kK, tb + p_col(b) + ks * 8, qm + Ly::moff(ks), id_o,
                      (i > 0 || ks > 0) ? 1u : 0u);
         }
-        tc::tc_commit(&bars[B_QEMPTY + st]);
-        tc::tc_commit(&bars[B_DONE + b]);
-        if (i == NT - 1) tc::tc_commit(&bars[B_ALL]);
+        commit32(sb + 8 * (B_QEMPTY + st));
+        commit32(sb + 8 * (B_DONE + b));
+        if (i == NT - 1) commit32(sb + 8 * (B_ALL));
       }
       __syncwarp();
       if (i + 2 < NT) ok = issue_s(i + 2);
     }
-    if (tc::elect_one()) tc::tc_commit(&bars[B_DRAIN]);
+    if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN));
     __syncwarp();
-    if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) set_status(P.status, PACK3D_ERR_TIMEOUT);
+    if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) *abort_flag = 1;
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort_flag) set_status(P.status, PACK3D_ERR_TIMEOUT);
   if (warp == 9) {
     __syncwarp();
     tc::tc_fence_after();
@@ -693,12 +730,10 @@ static cudaError_t launch_bwd(const Problem& p, const MaskTables& m, const void*
     return cudaErrorInvalidValue;
   const int64_t npad = (p.np + kTile - 1) / kTile * kTile;
   float2* rows = static_cast<float2*>(ws);
-  constexpr int per = 256 / (D <= 64 ? 8 : 16);
-  k_cross_rows<D><<<(unsigned)((p.bh * npad + per - 1) / per), 256, 0, p.s>>>(
-      static_cast<const __nv_bfloat16*>(dO), static_cast<const __nv_bfloat16*>(o), lse, p.np, npad,
-      p.bh, p.scale, rows);
   xb::Params P{};
   P.rows = rows;
+  P.o = static_cast<const __nv_bfloat16*>(o);
+  P.lse = lse;
   P.act = m.act;
   P.bits = m.bits;
   P.status = p.status;
@@ -733,7 +768,7 @@ static cudaError_t launch_bwd(const Problem& p, const MaskTables& m, const void*
   const int64_t items = p.bh * P.tiles * P.nsplit;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   k_cross_dkv<D><<<(unsigned)items, xk::kThreads, Sk::kBytes, p.s>>>(q64, g64, k128, v128, P);
-  count_launch(3);
+  count_launch(2);
   if (P.nsplit > 1) {
     const int64_t n = p.bh * p.l * D;
     k_cross_sum<<<dim3((unsigned)((n / 4 + 255) / 256), 2), 256, 0, p.s>>>(
