@@ -58,6 +58,10 @@ struct Params {
 // -------------------------------------------------------------------------------------- dq
 namespace xq {
 constexpr int kThreads = 256;  // elementwise 0-3, TMA 4, MMA 5, masked rows of K 6
+// Registers: two CTAs per SM leave 128 per thread at the launch; the elementwise warps, which hold
+// 64 columns of S and of dP, take 176, the others keep 80: 128 (176 + 80) = 256 * 128.
+constexpr int kRegs = 128, kMore = 176, kLess = 80;
+static_assert(128 * (kMore + kLess) <= kThreads * kRegs, "registers of the launch");
 template <int D> struct Smem {
   static constexpr int TB = Lay<D>::bytes(kTile), HB = Lay<D>::bytes(xb::kHalf);
   static constexpr int kQ = 0, kG = TB, kRing = 2 * TB;
@@ -154,6 +158,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
 
   if (warp < 4) {
     // ------------------------------------------------------------ elementwise and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMore));
     const int rin = warp * 32 + lane;
     const uint32_t tl = tbase + ((uint32_t)(warp * 32) << 16);
     uint32_t gc = 0, uc = 0, staged = 0;
@@ -202,20 +207,24 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
         if (!ok) break;
         tc::tc_fence_after();
         const uint32_t done = ab.probe(sb + 8 * (B_DONE), gc - 1);
+        uint32_t sv[2][32], dv[2][32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t sv[32], dv[32], pk[16];
-          tc::tmem_ld32(tl + C::kS + 32 * h, sv);
-          tc::tmem_ld32(tl + C::kP + 32 * h, dv);
-          tc::tmem_wait_ld();
-          if (C::kOwn && h == 1) {
-            tc::tc_fence_before();
-            arrive32(sb + 8 * (B_SFREE));
-          }
+          tc::tmem_ld32(tl + C::kS + 32 * h, sv[h]);
+          tc::tmem_ld32(tl + C::kP + 32 * h, dv[h]);
+        }
+        tc::tmem_wait_ld();
+        if (C::kOwn) {
+          tc::tc_fence_before();
+          arrive32(sb + 8 * (B_SFREE));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            const float2 x = tc::fma2(xb::f2(sv[k], sv[k + 1]), sl2, nl2);
-            const float2 t = tc::fma2(xb::f2(dv[k], dv[k + 1]), sc2, nd2);
+            const float2 x = tc::fma2(xb::f2(sv[h][k], sv[h][k + 1]), sl2, nl2);
+            const float2 t = tc::fma2(xb::f2(dv[h][k], dv[h][k + 1]), sc2, nd2);
             float2 ds = xb::mul2(make_float2(ex2(x.x), ex2(x.y)), t);
             if (w[h] != 0xffffffffu) {
               ds.x = ((w[h] >> k) & 1u) ? ds.x : 0.f;
@@ -229,7 +238,6 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
             if (!ok) break;
             tc::tc_fence_after();
           }
-          // (over S: columns that this thread has read)
           tc::tmem_st16(tl + C::kD + 16 * h, pk);
         }
         if (!ok) break;
@@ -283,7 +291,9 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
       ok = __all_sync(0xffffffffu, ok);  // a warp leaves the loop as one
     }
     if (rin == 0) bulk_wait();
-  } else if (warp == 4) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLess));
+  if (warp == 4) {
     // ------------------------------------------------------------ TMA loads
     if (lane == 0) {
       uint32_t kv = 0, uc = 0;
@@ -412,6 +422,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
       }
     }
   }
+  }
   tc::tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag) set_status(P.status, PACK3D_ERR_TIMEOUT);
@@ -424,26 +435,44 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
 
 // ---------------------------------------------------------------------------------- dk, dv
 namespace xk {
-constexpr int kThreads = 320;  // elementwise 0-3 (even steps), 4-7 (odd), TMA 8, MMA 9
+constexpr int kThreads = 384;  // elementwise 0-3 (even steps), 4-7 (odd), TMA 8, MMA 9
+// Registers: 168 per thread at the launch; the elementwise warps, which hold 64 columns of S^T and
+// of dP^T, take 208, the others keep 88: 256 * 208 + 128 * 88 = 384 * 168.
+constexpr int kRegs = 168, kMore = 208, kLess = 88;
+static_assert(256 * kMore + 128 * kLess <= kThreads * kRegs, "registers of the launch");
 template <int D> struct Smem {
   static constexpr int TB = Lay<D>::bytes(kTile), HB = Lay<D>::bytes(xb::kHalf);
   static constexpr int kK = 0, kV = TB, kRing = 2 * TB;
   static constexpr int kRowB = xb::kHalf * 8;               // (-lse log2(e), D tau) of a step's rows
-  static constexpr int kStages = 4;
+  static constexpr int kStages = D <= 96 ? 6 : 4;  // even: a group of warps sees the same slots
   static constexpr int kRows = kRing + kStages * 2 * HB;    // [stages]
   static constexpr int kBar = kRows + kStages * kRowB;
   static constexpr int kBytes = kBar + 512;
 };
-constexpr int kStages = 4;
+constexpr int kMaxStages = 6;
 enum {
-  B_AFULL = 0, B_QFULL = 1, B_QEMPTY = B_QFULL + kStages, B_SFULL = B_QEMPTY + kStages,
-  B_PFULL = B_SFULL + 2, B_DONE = B_PFULL + 2, B_ALL = B_DONE + 2, B_DRAIN, B_COUNT
+  B_AFULL = 0, B_QFULL = 1, B_QEMPTY = B_QFULL + kMaxStages, B_SFULL = B_QEMPTY + kMaxStages,
+  B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_DONE = B_PFULL + 2, B_ALL = B_DONE + 2, B_DRAIN, B_COUNT
 };
 static_assert(8 * B_COUNT + 16 <= 512, "barrier area");
-// TMEM columns: dk, dv; S^T and dP^T of step i in buffer i % 2
-constexpr uint32_t kK = 0, kV = 128;
-__device__ __forceinline__ uint32_t s_col(int b) { return 256u + 128u * b; }
-__device__ __forceinline__ uint32_t p_col(int b) { return 320u + 128u * b; }
+// TMEM columns: dk, dv and slots of 64. Step i has S^T in slot s(i), over which its P and dS (bf16)
+// go, and dP^T in slot g(i). With five slots (d <= 96) s(i) = i mod 5 and g(i) = s(i + 2): S^T of
+// step i + 2 goes where dP^T of step i has been read, dP^T where P and dS of step i - 1 were, so
+// that the products of steps i and i + 2 need not wait for one another. At d = 128 there are four:
+// steps i and i + 2 share theirs.
+template <int D> struct Cols {
+  static constexpr bool kFive = D <= 96;
+  static constexpr uint32_t kK = 0, kV = D, kS = 2 * D;
+  static_assert(kS + 64 * (kFive ? 5 : 4) <= 512, "tensor memory");
+  __device__ __forceinline__ static uint32_t s(int i) {
+    return kS + 64u * (kFive ? (uint32_t)i % 5u : 2u * ((uint32_t)i & 1u));
+  }
+  __device__ __forceinline__ static uint32_t g(int i) { return kFive ? s(i + 2) : s(i) + 64u; }
+  // P of 16 rows; dS 16 columns further
+  __device__ __forceinline__ static uint32_t p(int i, int ks) {
+    return s(i) + 32u * (ks >> 1) + 8u * (ks & 1);
+  }
+};
 }  // namespace xk
 
 template <int D>
@@ -454,6 +483,8 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
   using namespace xk;
   using S = Smem<D>;
   using Ly = Lay<D>;
+  using C = Cols<D>;
+  constexpr int kStages = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kBar + 8 * B_COUNT);
@@ -479,6 +510,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars[B_SFULL + i], 1);
+      tc::mbar_init(&bars[B_SFREE + i], 128);
       tc::mbar_init(&bars[B_PFULL + i], 128);
       tc::mbar_init(&bars[B_DONE + i], 1);
     }
@@ -495,41 +527,53 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------ elementwise and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMore));
     const int b = warp >> 2, rin = (warp & 3) * 32 + lane;
     const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     const float2 sl2 = make_float2(P.scale_log2, P.scale_log2);
     const float2 sc2 = make_float2(P.scale, P.scale);
     bool ok = true;
+    uint32_t seen = 0;
+#pragma unroll 1
     for (int i = b; i < NT; i += 2) {
-      if (!ab.all(sb + 8 * (B_SFULL + b), (i >> 1) & 1)) { ok = false; break; }
-      // the row data came with the step's tiles
-      if (!ab.all(sb + 8 * (B_QFULL + i % kStages), (i / kStages) & 1)) {
-        ok = false;
-        break;
-      }
+      // (the row data came with the step's tiles)
+      ok = ab.all(seen, sb + 8 * (B_SFULL + b), i >> 1) &&
+           ab.all(sb + 8 * (B_QFULL + i % kStages), i / kStages);
+      if (!ok) break;
       tc::tc_fence_after();
       // one 16-byte read brings two rows' data (every thread reads the same)
       const float4* rd =
           reinterpret_cast<const float4*>(smem + S::kRows + (i % kStages) * S::kRowB);
+      uint32_t sv[2][32], dv[2][32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t sv[32], dv[32], pp[16], pd[16];
-        tc::tmem_ld32(tl + s_col(b) + 32 * h, sv);
-        tc::tmem_ld32(tl + p_col(b) + 32 * h, dv);
-        tc::tmem_wait_ld();
+        tc::tmem_ld32(tl + C::s(i) + 32 * h, sv[h]);
+        tc::tmem_ld32(tl + C::g(i) + 32 * h, dv[h]);
+      }
+      tc::tmem_wait_ld();
+      if (C::kFive) {
+        tc::tc_fence_before();
+        arrive32(sb + 8 * (B_SFREE + b));
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pp[16], pd[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
           const float4 r = rd[16 * h + (k >> 1)];
-          const float2 x = tc::fma2(xb::f2(sv[k], sv[k + 1]), sl2, make_float2(r.x, r.z));
+          const float2 x =
+              tc::fma2(xb::f2(sv[h][k], sv[h][k + 1]), sl2, make_float2(r.x, r.z));
           const float2 p = make_float2(ex2(x.x), ex2(x.y));
-          const float2 t = tc::fma2(xb::f2(dv[k], dv[k + 1]), sc2, make_float2(-r.y, -r.w));
+          const float2 t =
+              tc::fma2(xb::f2(dv[h][k], dv[h][k + 1]), sc2, make_float2(-r.y, -r.w));
           const float2 ds = xb::mul2(p, t);
           pp[k >> 1] = tc::pack_bf16(p.x, p.y);
           pd[k >> 1] = tc::pack_bf16(ds.x, ds.y);
         }
-        tc::tmem_st16(tl + s_col(b) + 16 * h, pp);
-        tc::tmem_st16(tl + p_col(b) + 16 * h, pd);
+        tc::tmem_st16(tl + C::s(i) + 32 * h, pp);
+        tc::tmem_st16(tl + C::s(i) + 32 * h + 16, pd);
       }
+      seen = C::kFive ? ab.probe(sb + 8 * (B_SFULL + b), (i >> 1) + 1) : 0u;
       tc::tmem_wait_st();
       tc::tc_fence_before();
       arrive32(sb + 8 * (B_PFULL + b));
@@ -545,7 +589,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
       for (int c = 0; c < D; c += 16) {
         uint32_t a[16];
         if (NT > 0) {
-          tc::tmem_ld16(tl + (b ? kV : kK) + c, a);
+          tc::tmem_ld16(tl + (b ? C::kV : C::kK) + c, a);
           tc::tmem_wait_ld();
         }
         if (NT == 0 || !in)
@@ -572,7 +616,9 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
         }
       }
     }
-  } else if (warp == 8) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLess));
+  if (warp == 8) {
     // ------------------------------------------------------------ loads
     if (lane == 0 && NT > 0) {
       tc::mbar_expect_tx(&bars[B_AFULL], 2 * S::TB);
@@ -595,7 +641,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
       for (int k = i > kStages ? i - kStages : 0; k < i; ++k)
         tc::mbar_wait(&bars[B_QFULL + (k % kStages)], (k / kStages) & 1);
     }
-  } else {
+  } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
     const uint32_t id_s = tc::idesc_bf16_f32(128, xb::kHalf, false, false);
@@ -605,19 +651,22 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
     const uint64_t rk0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
     const uint64_t rm0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
     constexpr uint64_t HO = (uint64_t)(S::HB >> 4);
-    // S^T and dP^T of step i into buffer i % 2, free once step i - 2's products completed
+    // S^T and dP^T of step i, once those of step i - 2 have been read and the products of step i - 3
+    // have completed; with four slots, the products of step i - 2
     auto issue_s = [&](int i) -> bool {
       const int st = i % kStages, b = i & 1;
       if (!ab.all(sb + 8 * (B_QFULL + st), (i / kStages) & 1)) return false;
-      if (i >= 2 && !ab.all(sb + 8 * (B_DONE + b), ((i - 2) >> 1) & 1)) return false;
+      const int done = i - (C::kFive ? 3 : 2);
+      if (C::kFive && i >= 2 && !ab.all(sb + 8 * (B_SFREE + b), (i - 2) >> 1)) return false;
+      if (done >= 0 && !ab.all(sb + 8 * (B_DONE + (done & 1)), done >> 1)) return false;
       tc::tc_fence_after();
       if (tc::elect_one()) {
         const uint64_t qo = rk0 + 2 * st * HO, go = qo + HO;
 #pragma unroll
         for (int ks = 0; ks < Ly::kSteps; ++ks) {
-          tc::mma_ss(tb + s_col(b), kd + Ly::koff(kTile, ks), qo + Ly::koff(xb::kHalf, ks), id_s,
+          tc::mma_ss(tb + C::s(i), kd + Ly::koff(kTile, ks), qo + Ly::koff(xb::kHalf, ks), id_s,
                      ks > 0);
-          tc::mma_ss(tb + p_col(b), vd + Ly::koff(kTile, ks), go + Ly::koff(xb::kHalf, ks), id_s,
+          tc::mma_ss(tb + C::g(i), vd + Ly::koff(kTile, ks), go + Ly::koff(xb::kHalf, ks), id_s,
                      ks > 0);
         }
         commit32(sb + 8 * (B_SFULL + b));
@@ -629,15 +678,16 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
     for (int i = 0; i < 2 && i < NT && ok; ++i) ok = issue_s(i);
     for (int i = 0; i < NT && ok; ++i) {
       const int st = i % kStages, b = i & 1;
+      if (C::kFive && i + 2 < NT && !issue_s(i + 2)) break;
       if (!ab.all(sb + 8 * (B_PFULL + b), (i >> 1) & 1)) break;
       tc::tc_fence_after();
       if (tc::elect_one()) {
         const uint64_t qm = rm0 + 2 * st * HO, gm = qm + HO;
 #pragma unroll
         for (int ks = 0; ks < xb::kHalf / 16; ++ks) {
-          tc::mma_ts(tb + kV, tb + s_col(b) + ks * 8, gm + Ly::moff(ks), id_o,
+          tc::mma_ts(tb + C::kV, tb + C::p(i, ks), gm + Ly::moff(ks), id_o,
                      (i > 0 || ks > 0) ? 1u : 0u);
-          tc::mma_ts(tb + kK, tb + p_col(b) + ks * 8, qm + Ly::moff(ks), id_o,
+          tc::mma_ts(tb + C::kK, tb + C::p(i, ks) + 16u, qm + Ly::moff(ks), id_o,
                      (i > 0 || ks > 0) ? 1u : 0u);
         }
         commit32(sb + 8 * (B_QEMPTY + st));
@@ -645,11 +695,12 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
         if (i == NT - 1) commit32(sb + 8 * (B_ALL));
       }
       __syncwarp();
-      if (i + 2 < NT) ok = issue_s(i + 2);
+      if (!C::kFive && i + 2 < NT) ok = issue_s(i + 2);
     }
     if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN));
     __syncwarp();
     if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) *abort_flag = 1;
+  }
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -717,6 +768,14 @@ static cudaError_t launch_bwd(const Problem& p, const MaskTables& m, const void*
   if (e == cudaSuccess)
     e = smem_attr_once(reinterpret_cast<const void*>(k_cross_dkv<D>), Sk::kBytes, ak);
   if (e != cudaSuccess) return e;
+  // the split of registers needs every one of the launch's
+  static const bool split_fits = [] {
+    cudaFuncAttributes a, b;
+    return cudaFuncGetAttributes(&a, k_cross_dq<D>) == cudaSuccess &&
+           cudaFuncGetAttributes(&b, k_cross_dkv<D>) == cudaSuccess && a.numRegs >= xq::kRegs &&
+           b.numRegs >= xk::kRegs;
+  }();
+  if (!split_fits) return cudaErrorLaunchOutOfResources;
   CUtensorMap q128, g128, k64, v64, o128, q64, g64, k128, v128;
   if (!encode_rows<D>(&q128, p.q, p.np, p.bh, kTile) ||
       !encode_rows<D>(&g128, dO, p.np, p.bh, kTile) ||
