@@ -57,7 +57,7 @@ struct Params {
 
 // -------------------------------------------------------------------------------------- dq
 namespace xq {
-constexpr int kThreads = 256;  // elementwise 0-3, TMA 4, MMA 5, masked rows of K 6
+constexpr int kThreads = 256;  // elementwise 0-3, TMA 4, S and dP 5, masked rows of K 6, dq 7
 // Registers: two CTAs per SM leave 128 per thread at the launch; the elementwise warps, which hold
 // 64 columns of S and of dP, take 176, the others keep 80: 128 (176 + 80) = 256 * 128.
 constexpr int kRegs = 128, kMore = 176, kLess = 80;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
     tc::mbar_init(&bars[B_PFULL], 128);
     tc::mbar_init(&bars[B_DONE], 1);
     tc::mbar_init(&bars[B_STAGED], 128);
-    tc::mbar_init(&bars[B_DRAIN], 1);
+    tc::mbar_init(&bars[B_DRAIN], 2);
     abort_flag[0] = 0;
     tc::fence_mbar_init();
   }
@@ -325,54 +325,61 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
       if (uc) tc::mbar_wait(&bars[B_QFULL], (uc - 1) & 1);
     }
   } else if (warp == 5) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ S and dP
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
     const uint32_t id_s = tc::idesc_bf16_f32(128, xb::kHalf, false, false);
-    const uint32_t id_o = tc::idesc_bf16_f32(128, D, false, true);
     const uint64_t qd = Ly::kdesc(tc::smem_u32(smem + S::kQ));
     const uint64_t gd = Ly::kdesc(tc::smem_u32(smem + S::kG));
     const uint64_t kd0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
-    const uint64_t km0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
     const bool masked = P.act != nullptr;
-    uint32_t gc = 0, uc = 0;
+    uint32_t g = 0, uc = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
       const Unit U(P, u);
       if (!U.n) continue;
       if (!ab.all(sb + 8 * (B_QFULL), uc & 1)) break;
       ++uc;
-      // step i: S and dP of step i, then (one step later where dS has columns of its own) dq += dS K
-      constexpr int kLag = C::kOwn ? 1 : 0;
 #pragma unroll 1
-      for (int i = 0; i < U.n + kLag && ok; ++i) {
-        if (i < U.n) {
-          const uint32_t kv = 2 * (gc + i), g = gc + i;  // V and K of the step
-          const int sv = kv % NS, sk = (kv + 1) % NS;
-          ok = masked ? ab.all(sb + 8 * (B_READY + g % kReady), g / kReady)
-                      : ab.all(sb + 8 * (B_FULL + sk), (kv + 1) / NS);
-          ok = ok && ab.all(sb + 8 * (B_FULL + sv), kv / NS);
-          // S and dP have been read (and with dS over S: its product has completed)
-          if (g >= 1) ok = ok && ab.all(sb + 8 * (C::kOwn ? B_SFREE : B_DONE), g - 1);
-          if (!ok) break;
-          tc::tc_fence_after();
+      for (int j = 0; j < U.n; ++j, ++g) {
+        const int sv = 2 * g % NS, sk = (2 * g + 1) % NS;
+        ok = masked ? ab.all(sb + 8 * (B_READY + g % kReady), g / kReady)
+                    : ab.all(sb + 8 * (B_FULL + sk), (2 * g + 1) / NS);
+        ok = ok && ab.all(sb + 8 * (B_FULL + sv), 2 * g / NS);
+        // the last step's S and dP have been read (with dS over S: its product has completed)
+        if (g >= 1) ok = ok && ab.all(sb + 8 * (C::kOwn ? B_SFREE : B_DONE), g - 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
           const uint64_t ko = (uint64_t)((sk * S::HB) >> 4), vo = (uint64_t)((sv * S::HB) >> 4);
-          if (tc::elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < Ly::kSteps; ++ks) {
-              tc::mma_ss(tb + C::kS, qd + Ly::koff(kTile, ks), kd0 + ko + Ly::koff(xb::kHalf, ks),
-                         id_s, ks > 0);
-              tc::mma_ss(tb + C::kP, gd + Ly::koff(kTile, ks), kd0 + vo + Ly::koff(xb::kHalf, ks),
-                         id_s, ks > 0);
-            }
-            commit32(sb + 8 * (B_SFULL));
-            commit32(sb + 8 * (B_EMPTY + sv));
+          for (int ks = 0; ks < Ly::kSteps; ++ks) {
+            tc::mma_ss(tb + C::kS, qd + Ly::koff(kTile, ks), kd0 + ko + Ly::koff(xb::kHalf, ks),
+                       id_s, ks > 0);
+            tc::mma_ss(tb + C::kP, gd + Ly::koff(kTile, ks), kd0 + vo + Ly::koff(xb::kHalf, ks),
+                       id_s, ks > 0);
           }
-          __syncwarp();
+          commit32(sb + 8 * (B_SFULL));
+          commit32(sb + 8 * (B_EMPTY + sv));
         }
-        const int j = i - kLag;
-        if (j < 0) continue;
-        const int sk = (2 * (gc + j) + 1) % NS;
-        ok = ab.all(sb + 8 * (B_PFULL), gc + j);
+        __syncwarp();
+      }
+    }
+    if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN));
+    __syncwarp();
+    if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) *abort_flag = 1;
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ dq += dS K
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+    const uint32_t id_o = tc::idesc_bf16_f32(128, D, false, true);
+    const uint64_t km0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
+    uint32_t g = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < P.units && ok; u += gridDim.x) {
+      const Unit U(P, u);
+#pragma unroll 1
+      for (int j = 0; j < U.n; ++j, ++g) {
+        const int sk = (2 * g + 1) % NS;
+        ok = ab.all(sb + 8 * (B_PFULL), g);
         if (!ok) break;
         tc::tc_fence_after();
         if (tc::elect_one()) {
@@ -386,7 +393,6 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
         }
         __syncwarp();
       }
-      gc += U.n;
     }
     if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN));
     __syncwarp();
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
 
 // ---------------------------------------------------------------------------------- dk, dv
 namespace xk {
-constexpr int kThreads = 384;  // elementwise 0-3 (even steps), 4-7 (odd), TMA 8, MMA 9
+constexpr int kThreads = 384;  // elementwise 0-3 (even steps), 4-7 (odd), TMA 8, S and dP 9, dk and dv 10
 // Registers: 168 per thread at the launch; the elementwise warps, which hold 64 columns of S^T and
 // of dP^T, take 208, the others keep 88: 256 * 208 + 128 * 88 = 384 * 168.
 constexpr int kRegs = 168, kMore = 208, kLess = 88;
@@ -515,7 +521,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
       tc::mbar_init(&bars[B_DONE + i], 1);
     }
     tc::mbar_init(&bars[B_ALL], 1);
-    tc::mbar_init(&bars[B_DRAIN], 1);
+    tc::mbar_init(&bars[B_DRAIN], 2);
     abort_flag[0] = 0;
     tc::fence_mbar_init();
   }
@@ -642,26 +648,27 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
         tc::mbar_wait(&bars[B_QFULL + (k % kStages)], (k / kStages) & 1);
     }
   } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ S^T and dP^T
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
     const uint32_t id_s = tc::idesc_bf16_f32(128, xb::kHalf, false, false);
-    const uint32_t id_o = tc::idesc_bf16_f32(128, D, false, true);
     const uint64_t kd = Ly::kdesc(tc::smem_u32(smem + S::kK));
     const uint64_t vd = Ly::kdesc(tc::smem_u32(smem + S::kV));
-    const uint64_t rk0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
-    const uint64_t rm0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
+    const uint64_t r0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
     constexpr uint64_t HO = (uint64_t)(S::HB >> 4);
-    // S^T and dP^T of step i, once those of step i - 2 have been read and the products of step i - 3
-    // have completed; with four slots, the products of step i - 2
-    auto issue_s = [&](int i) -> bool {
+    bool ok = NT > 0 && ab.all(sb + 8 * (B_AFULL), 0);
+#pragma unroll 1
+    for (int i = 0; i < NT && ok; ++i) {
       const int st = i % kStages, b = i & 1;
-      if (!ab.all(sb + 8 * (B_QFULL + st), (i / kStages) & 1)) return false;
+      ok = ab.all(sb + 8 * (B_QFULL + st), i / kStages);
+      // once those of step i - 2 have been read and the products of step i - 3 have completed; with
+      // four slots, the products of step i - 2
       const int done = i - (C::kFive ? 3 : 2);
-      if (C::kFive && i >= 2 && !ab.all(sb + 8 * (B_SFREE + b), (i - 2) >> 1)) return false;
-      if (done >= 0 && !ab.all(sb + 8 * (B_DONE + (done & 1)), done >> 1)) return false;
+      if (C::kFive && i >= 2) ok = ok && ab.all(sb + 8 * (B_SFREE + b), (i - 2) >> 1);
+      if (done >= 0) ok = ok && ab.all(sb + 8 * (B_DONE + (done & 1)), done >> 1);
+      if (!ok) break;
       tc::tc_fence_after();
       if (tc::elect_one()) {
-        const uint64_t qo = rk0 + 2 * st * HO, go = qo + HO;
+        const uint64_t qo = r0 + 2 * st * HO, go = qo + HO;
 #pragma unroll
         for (int ks = 0; ks < Ly::kSteps; ++ks) {
           tc::mma_ss(tb + C::s(i), kd + Ly::koff(kTile, ks), qo + Ly::koff(xb::kHalf, ks), id_s,
@@ -672,17 +679,23 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
         commit32(sb + 8 * (B_SFULL + b));
       }
       __syncwarp();
-      return true;
-    };
-    bool ok = NT > 0 && ab.all(sb + 8 * (B_AFULL), 0);
-    for (int i = 0; i < 2 && i < NT && ok; ++i) ok = issue_s(i);
-    for (int i = 0; i < NT && ok; ++i) {
+    }
+    if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN));
+    __syncwarp();
+    if (!tc::mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) *abort_flag = 1;
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ dv += P^T dO, dk += dS^T q
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+    const uint32_t id_o = tc::idesc_bf16_f32(128, D, false, true);
+    const uint64_t r0 = Ly::mdesc(tc::smem_u32(smem + S::kRing), xb::kHalf);
+    constexpr uint64_t HO = (uint64_t)(S::HB >> 4);
+#pragma unroll 1
+    for (int i = 0; i < NT; ++i) {
       const int st = i % kStages, b = i & 1;
-      if (C::kFive && i + 2 < NT && !issue_s(i + 2)) break;
-      if (!ab.all(sb + 8 * (B_PFULL + b), (i >> 1) & 1)) break;
+      if (!ab.all(sb + 8 * (B_PFULL + b), i >> 1)) break;
       tc::tc_fence_after();
       if (tc::elect_one()) {
-        const uint64_t qm = rm0 + 2 * st * HO, gm = qm + HO;
+        const uint64_t qm = r0 + 2 * st * HO, gm = qm + HO;
 #pragma unroll
         for (int ks = 0; ks < xb::kHalf / 16; ++ks) {
           tc::mma_ts(tb + C::kV, tb + C::p(i, ks), gm + Ly::moff(ks), id_o,
@@ -695,7 +708,6 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
         if (i == NT - 1) commit32(sb + 8 * (B_ALL));
       }
       __syncwarp();
-      if (!C::kFive && i + 2 < NT) ok = issue_s(i + 2);
     }
     if (tc::elect_one()) commit32(sb + 8 * (B_DRAIN));
     __syncwarp();
