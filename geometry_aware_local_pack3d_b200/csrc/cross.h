@@ -66,6 +66,15 @@ cudaError_t build_mask(const Problem& p, const MaskTables& m);
 size_t fwd_tc_bytes(const Problem& p);
 cudaError_t fwd_tc(const Problem& p, const MaskTables& m, void* o, float* lse, void* ws);
 cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse);
+// bf16 forward of few rows (no mask tables)
+bool few_fwd(const Problem& p);
+size_t few_bytes(const Problem& p);
+cudaError_t fwd_few(const Problem& p, void* o, float* lse, void* ws);
+// o and lse of rows whose states went to `nsplit` ranges: part_o [nsplit][rows][d], part_lse
+// [nsplit][rows]
+constexpr int kMaxSplits = 160;
+cudaError_t join_splits(const Problem& p, const float* part_o, const float* part_lse, int nsplit,
+                        void* o, float* lse);
 // bf16 forward and backward of a short context (no mask tables)
 bool short_fwd(const Problem& p);
 cudaError_t fwd_short(const Problem& p, void* o, float* lse);
@@ -85,6 +94,11 @@ cudaError_t bwd_simt(const Problem& p, const MaskTables& m, const void* o, const
 template <int W>
 __device__ __forceinline__ void state_words(const uint32_t* bits, int64_t l, int64_t at,
                                             uint32_t (&w)[W]) {
+  if (!bits && at + 32 * W <= l) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0xffffffffu;
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     if (bits) {

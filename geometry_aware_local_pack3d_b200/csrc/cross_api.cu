@@ -55,6 +55,7 @@ pack3d_status make(xa::Problem* p, int dtype, int batch, int heads, int kv_heads
 size_t bytes_of(const xa::Problem& p, bool mask, bool backward) {
   if (p.l == 0 || p.np == 0) return 0;
   if (backward ? xa::short_bwd(p) : xa::short_fwd(p)) return backward ? xa::bwd_short_bytes(p) : 0;
+  if (!backward && xa::few_fwd(p)) return xa::few_bytes(p);
   const bool tc = p.dtype == PACK3D_BF16;
   const size_t own = backward ? (tc ? xa::bwd_tc_bytes(p) : xa::bwd_simt_bytes(p))
                               : (tc ? xa::fwd_tc_bytes(p) : 0);
@@ -111,6 +112,7 @@ extern "C" pack3d_status pack3d_cross_attn_fwd(const void* q, const void* k, con
     return cuda_status(empty_rows(o, rows * p.d * (dtype == PACK3D_BF16 ? 2 : 4), lse, rows, p.s));
   if ((st = check_workspace(p, workspace, workspace_bytes, false)) != PACK3D_OK) return st;
   if (xa::short_fwd(p)) return cuda_status(xa::fwd_short(p, o, lse));
+  if (xa::few_fwd(p)) return cuda_status(xa::fwd_few(p, o, lse, workspace));
   const int tw = xa::mask_tile_words(p, false);
   const xa::MaskTables m = xa::mask_at(p, tw, workspace);
   cudaError_t e = xa::build_mask(p, m);

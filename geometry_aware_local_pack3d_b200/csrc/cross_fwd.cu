@@ -620,7 +620,6 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
 // Joins the splits of each row: lse = log sum_s exp(lse_s), o = sum_s exp(lse_s - lse) o_s, in
 // split order. A warp per row, four columns per lane; the weights first, so that the loop over the
 // splits is independent loads.
-constexpr int kMaxSplits = 160;
 template <int D>
 __global__ void __launch_bounds__(128)
     k_cross_join(const float* __restrict__ part_o, const float* __restrict__ part_lse, int nsplit,
@@ -665,6 +664,21 @@ __global__ void __launch_bounds__(128)
         tc::pack_bf16(a.x * inv, a.y * inv), tc::pack_bf16(a.z * inv, a.w * inv));
   }
   if (lse && lane == 0) lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
+}
+
+cudaError_t join_splits(const Problem& p, const float* part_o, const float* part_lse, int nsplit,
+                        void* o, float* lse) {
+  const int64_t rows = p.bh * p.np;
+  const unsigned grid = (unsigned)((rows + 3) / 4);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(o);
+  switch (p.d) {
+    case 48: k_cross_join<48><<<grid, 128, 0, p.s>>>(part_o, part_lse, nsplit, rows, out, lse); break;
+    case 64: k_cross_join<64><<<grid, 128, 0, p.s>>>(part_o, part_lse, nsplit, rows, out, lse); break;
+    case 96: k_cross_join<96><<<grid, 128, 0, p.s>>>(part_o, part_lse, nsplit, rows, out, lse); break;
+    default: k_cross_join<128><<<grid, 128, 0, p.s>>>(part_o, part_lse, nsplit, rows, out, lse);
+  }
+  count_launch();
+  return cudaGetLastError();
 }
 
 // One block per batch entry: the bits and the list of tiles with an unmasked state.
@@ -792,12 +806,7 @@ static cudaError_t launch_fwd(const Problem& p, const MaskTables& m, void* o, fl
   k_cross_fwd<D><<<grid, xf::kThreads, S::kBytes, p.s>>>(
       mq, mk, mv, mo, P);
   count_launch();
-  if (P.nsplit > 1) {
-    const int64_t rows = p.bh * p.np;
-    k_cross_join<D><<<(unsigned)((rows + 3) / 4), 128, 0, p.s>>>(P.part_o, P.part_lse, P.nsplit,
-                                                               rows, P.o, lse);
-    count_launch();
-  }
+  if (P.nsplit > 1) return join_splits(p, P.part_o, P.part_lse, P.nsplit, o, lse);
   return cudaGetLastError();
 }
 

@@ -86,6 +86,16 @@ def test_few_rows_over_a_long_context(B, H, HK, N, L, mask):
     assert torch.equal(f["o"], again["o"]) and torch.equal(f["lse"], again["lse"])
 
 
+@pytest.mark.parametrize("d", [48, 64, 96, 128])
+@pytest.mark.parametrize("B,H,HK,N,L,mask", [
+    (2, 6, 3, 8, 129, "random"),     # 16 rows, the largest count with a kernel of its own
+    (1, 17, 1, 1, 300, "pad"),       # 17 rows: the general one
+    (3, 5, 1, 1, 4099, "left"), (2, 2, 2, 2, 1024, "empty"),
+    (40, 8, 8, 1, 4500, "random")])  # more states than a warp lists at once, one block per problem
+def test_rows_of_single_tokens(d, B, H, HK, N, L, mask):
+    run_and_check(*make(B, H, HK, N, L, d, torch.bfloat16, mask, garbage=True), backward=False)
+
+
 def test_many_units_per_cta_and_split_row_ranges():
     # more 256-row units than SMs, a last unit of one tile, key gradients over several ranges
     run_and_check(*make(2, 4, 4, 8192 + 100, 260, 96, torch.bfloat16, "pad", seed=7))

@@ -14,7 +14,7 @@ FAKE, ODD = 0x100000, 0x100004
 
 
 def cross_fwd(**kw):
-    a = dict(q=FAKE, k=FAKE, v=FAKE, mask=None, dtype=1, batch=1, heads=2, kv_heads=2, n=10, l=200, d=96,
+    a = dict(q=FAKE, k=FAKE, v=FAKE, mask=None, dtype=1, batch=1, heads=2, kv_heads=2, n=20, l=200, d=96,
              scale=0.1, o=FAKE, lse=None, ws=None, bytes=0, status=None)
     a.update(kw)
     return b.lib().pack3d_cross_attn_fwd(a["q"], a["k"], a["v"], a["mask"], a["dtype"], a["batch"],
