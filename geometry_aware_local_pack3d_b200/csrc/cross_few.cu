@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(32 * fw::Cfg<D>::kWarps, 2) k_cross_few(const 
   const __nv_bfloat16 *k = P.k + bh * P.l * D, *v = P.v + bh * P.l * D;
   const uint8_t* mask = P.mask ? P.mask + bh / P.kv_heads * P.l : nullptr;
   const uint32_t buf = tc::smem_u32(smem) + warp * 2 * C::kStage;
+  // the join may be launched; it waits for this kernel's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint32_t qa[KS][4];
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks)

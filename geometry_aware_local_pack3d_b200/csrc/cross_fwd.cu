@@ -617,17 +617,19 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
   }
 }
 
-// Joins the splits of each row: lse = log sum_s exp(lse_s), o = sum_s exp(lse_s - lse) o_s, in
-// split order. A warp per row, four columns per lane; the weights first, so that the loop over the
-// splits is independent loads.
+// Joins the splits of each row: lse = log sum_s exp(lse_s), o = sum_s exp(lse_s - lse) o_s. A block
+// per row: every warp forms the weights (a few loads), sums every fourth split, four columns per
+// lane, and the four sums are added in order. Latency is all of it: it is launched while the kernel
+// before it still runs and waits for that kernel's end here.
 template <int D>
 __global__ void __launch_bounds__(128)
     k_cross_join(const float* __restrict__ part_o, const float* __restrict__ part_lse, int nsplit,
                  int64_t rows, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
   __shared__ float wgt[4][kMaxSplits];
+  __shared__ float4 sums[4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x * 4ll + warp;
-  if (row >= rows) return;
+  const int64_t row = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float top = -INFINITY;
   for (int s = lane; s < nsplit; s += 32) {
     const float x = part_lse[s * rows + row];
@@ -646,11 +648,10 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   __syncwarp();
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   if (lane < D / 4) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int s = 0; s < nsplit; ++s) {
+#pragma unroll 5
+    for (int s = warp; s < nsplit; s += 4) {
       const float f = wgt[warp][s];
       // a split without any state has written no row
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -660,25 +661,48 @@ __global__ void __launch_bounds__(128)
       a.z = fmaf(f, x.z, a.z);
       a.w = fmaf(f, x.w, a.w);
     }
+    sums[warp][lane] = a;
+  }
+  __syncthreads();
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (threadIdx.x < D / 4) {
+    float4 a = sums[0][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      const float4 x = sums[w][lane];
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    }
     *reinterpret_cast<uint2*>(o + row * D + 4 * lane) = make_uint2(
         tc::pack_bf16(a.x * inv, a.y * inv), tc::pack_bf16(a.z * inv, a.w * inv));
   }
-  if (lse && lane == 0) lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
+  if (lse && threadIdx.x == 0) lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
+}
+
+template <int D>
+static cudaError_t launch_join(const Problem& p, const float* part_o, const float* part_lse,
+                               int nsplit, void* o, float* lse) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)(p.bh * p.np));
+  c.blockDim = dim3(128);
+  c.stream = p.s;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&c, k_cross_join<D>, part_o, part_lse, nsplit, p.bh * p.np,
+                            static_cast<__nv_bfloat16*>(o), lse);
 }
 
 cudaError_t join_splits(const Problem& p, const float* part_o, const float* part_lse, int nsplit,
                         void* o, float* lse) {
-  const int64_t rows = p.bh * p.np;
-  const unsigned grid = (unsigned)((rows + 3) / 4);
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(o);
   switch (p.d) {
-    case 48: k_cross_join<48><<<grid, 128, 0, p.s>>>(part_o, part_lse, nsplit, rows, out, lse); break;
-    case 64: k_cross_join<64><<<grid, 128, 0, p.s>>>(part_o, part_lse, nsplit, rows, out, lse); break;
-    case 96: k_cross_join<96><<<grid, 128, 0, p.s>>>(part_o, part_lse, nsplit, rows, out, lse); break;
-    default: k_cross_join<128><<<grid, 128, 0, p.s>>>(part_o, part_lse, nsplit, rows, out, lse);
+    case 48: return launch_join<48>(p, part_o, part_lse, nsplit, o, lse);
+    case 64: return launch_join<64>(p, part_o, part_lse, nsplit, o, lse);
+    case 96: return launch_join<96>(p, part_o, part_lse, nsplit, o, lse);
+    default: return launch_join<128>(p, part_o, part_lse, nsplit, o, lse);
   }
-  count_launch();
-  return cudaGetLastError();
 }
 
 // One block per batch entry: the bits and the list of tiles with an unmasked state.
