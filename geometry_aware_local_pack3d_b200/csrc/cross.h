@@ -65,7 +65,8 @@ cudaError_t build_mask(const Problem& p, const MaskTables& m);
 // forward (o, lse), bf16 and fp32; `ws` follows the mask's tables
 size_t fwd_tc_bytes(const Problem& p);
 cudaError_t fwd_tc(const Problem& p, const MaskTables& m, void* o, float* lse, void* ws);
-cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse);
+size_t fwd_simt_bytes(const Problem& p);
+cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse, void* ws);
 // bf16 forward of few rows (no mask tables)
 bool few_fwd(const Problem& p);
 size_t few_bytes(const Problem& p);

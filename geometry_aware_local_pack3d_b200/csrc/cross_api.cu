@@ -58,7 +58,7 @@ size_t bytes_of(const xa::Problem& p, bool mask, bool backward) {
   if (!backward && xa::few_fwd(p)) return xa::few_bytes(p);
   const bool tc = p.dtype == PACK3D_BF16;
   const size_t own = backward ? (tc ? xa::bwd_tc_bytes(p) : xa::bwd_simt_bytes(p))
-                              : (tc ? xa::fwd_tc_bytes(p) : 0);
+                              : (tc ? xa::fwd_tc_bytes(p) : xa::fwd_simt_bytes(p));
   return own + (mask ? xa::mask_bytes(p, xa::mask_tile_words(p, backward)) : 0);
 }
 
@@ -118,7 +118,7 @@ extern "C" pack3d_status pack3d_cross_attn_fwd(const void* q, const void* k, con
   cudaError_t e = xa::build_mask(p, m);
   if (e == cudaSuccess)
     e = dtype == PACK3D_BF16 ? xa::fwd_tc(p, m, o, lse, after_mask(p, tw, workspace))
-                             : xa::fwd_simt(p, m, o, lse);
+                             : xa::fwd_simt(p, m, o, lse, after_mask(p, tw, workspace));
   return cuda_status(e);
 }
 

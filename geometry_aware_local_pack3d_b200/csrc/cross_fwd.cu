@@ -621,10 +621,10 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
 // per row: every warp forms the weights (a few loads), sums every fourth split, four columns per
 // lane, and the four sums are added in order. Latency is all of it: it is launched while the kernel
 // before it still runs and waits for that kernel's end here.
-template <int D>
+template <int D, typename T>
 __global__ void __launch_bounds__(128)
     k_cross_join(const float* __restrict__ part_o, const float* __restrict__ part_lse, int nsplit,
-                 int64_t rows, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+                 int64_t rows, T* __restrict__ o, float* __restrict__ lse) {
   __shared__ float wgt[4][kMaxSplits];
   __shared__ float4 sums[4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -672,8 +672,12 @@ __global__ void __launch_bounds__(128)
       const float4 x = sums[w][lane];
       a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
     }
-    *reinterpret_cast<uint2*>(o + row * D + 4 * lane) = make_uint2(
-        tc::pack_bf16(a.x * inv, a.y * inv), tc::pack_bf16(a.z * inv, a.w * inv));
+    a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(o + row * D + 4 * lane) =
+          make_uint2(tc::pack_bf16(a.x, a.y), tc::pack_bf16(a.z, a.w));
+    else
+      *reinterpret_cast<float4*>(o + row * D + 4 * lane) = a;
   }
   if (lse && threadIdx.x == 0) lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
 }
@@ -691,8 +695,12 @@ static cudaError_t launch_join(const Problem& p, const float* part_o, const floa
   c.attrs = &early;
   c.numAttrs = 1;
   count_launch();
-  return cudaLaunchKernelEx(&c, k_cross_join<D>, part_o, part_lse, nsplit, p.bh * p.np,
-                            static_cast<__nv_bfloat16*>(o), lse);
+  const int64_t rows = p.bh * p.np;
+  return p.dtype == PACK3D_BF16
+             ? cudaLaunchKernelEx(&c, k_cross_join<D, __nv_bfloat16>, part_o, part_lse, nsplit, rows,
+                                  static_cast<__nv_bfloat16*>(o), lse)
+             : cudaLaunchKernelEx(&c, k_cross_join<D, float>, part_o, part_lse, nsplit, rows,
+                                  static_cast<float*>(o), lse);
 }
 
 cudaError_t join_splits(const Problem& p, const float* part_o, const float* part_lse, int nsplit,

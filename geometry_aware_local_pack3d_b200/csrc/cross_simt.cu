@@ -5,11 +5,15 @@
 // and states tx + 16 j of a score tile. What bounds it: the FMA pipe; a thread's 4 x 4 scores take
 // 64 FMAs per 8 shared loads of 16 bytes. The rows of a masked state are read as zeros, so that
 // nothing they hold reaches a product, and their scores are -inf.
-//   k_cross_fwd32   online softmax over the state tiles, o and lse
-//   k_cross_dq32    dq_i = sum_j dS_ij k_j,            dS = p (dO v - D) tau
+//   k_cross_fwd32   online softmax over a range of the state tiles, o and lse
+//   k_cross_dq32    dq_i = sum_j dS_ij k_j,            dS = p (dO v - D) tau, over such a range
 //   k_cross_dkv32   dk_j = sum_i dS_ij q_i,  dv_j = sum_i p_ij dO_i over a range of row tiles; the
 //                   ranges' sums are added in order by k_cross_sum
-// Every sum runs in a fixed order (no atomics).
+// The state ranges (one, unless the row tiles leave SMs idle) are joined by k_cross_join (o, lse) and
+// k_cross_sum32 (dq). Every sum runs in a fixed order (no atomics). A tile's 64 products are summed
+// apart and then added: one sum over 16,384 states or 65,536 rows would lose three bits to its order.
+// exp(s tau - lse) is formed as written, not as 2^(s tau log2 e - lse log2 e), whose rounded second
+// term would move a whole row's probabilities.
 #include <math.h>
 
 #include "cross.h"
@@ -66,10 +70,26 @@ __device__ __forceinline__ void product(const float* a, const float* b, int ty, 
   }
 }
 
+template <int D> __device__ __forceinline__ void clear(float (&a)[4][D / 16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) a[i][c] = 0.f;
+}
+template <int D>
+__device__ __forceinline__ void add(float (&acc)[4][D / 16], const float (&a)[4][D / 16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) acc[i][c] += a[i][c];
+}
+
 // acc[i][c] += sum over the 64 inner rows of m[4 ty + i][inner] b[inner][tx + 16 c]
 template <int D>
 __device__ __forceinline__ void accumulate(const float* m, const float* b, int ty, int tx,
-                                           float (&acc)[4][D / 16]) {
+                                           float (&out)[4][D / 16]) {
+  float acc[4][D / 16];
+  clear<D>(acc);
 #pragma unroll 2
   for (int k = 0; k < kT; k += 4) {
     float4 x[4];
@@ -87,12 +107,15 @@ __device__ __forceinline__ void accumulate(const float* m, const float* b, int t
       }
     }
   }
+  add<D>(out, acc);
 }
 
 // As accumulate with m transposed: acc[i][c] += sum over rows r of m[r][4 ty + i] b[r][tx + 16 c]
 template <int D>
 __device__ __forceinline__ void accumulate_t(const float* m, const float* b, int ty, int tx,
-                                             float (&acc)[4][D / 16]) {
+                                             float (&out)[4][D / 16]) {
+  float acc[4][D / 16];
+  clear<D>(acc);
 #pragma unroll 4
   for (int r = 0; r < kT; ++r) {
     const float4 x = *reinterpret_cast<const float4*>(m + r * kP + 4 * ty);
@@ -105,6 +128,7 @@ __device__ __forceinline__ void accumulate_t(const float* m, const float* b, int
       acc[3][c] = fmaf(x.w, y, acc[3][c]);
     }
   }
+  add<D>(out, acc);
 }
 
 __device__ __forceinline__ float row_max(float v) {
@@ -122,12 +146,14 @@ struct Params {
   const float *q, *k, *v, *dO, *o;
   const float *lse;       // backward
   float *out, *out_lse;   // o, lse  |  dq
+  float *part, *part_lse;  // of nstate > 1 state ranges: o or dq [nstate][rows][D], lse
   float *dk, *dv;         // partial sums [nsplit][bh][l][D]
   float *delta;           // [bh][np]
   const int32_t* act;
   const uint32_t* bits;
   int64_t np, l, bh, words;
-  int tiles, kv_heads, nsplit;
+  int tiles, kv_heads;
+  int nstate, nsplit;  // state ranges (o, dq); row ranges (dk, dv)
   float scale;
 };
 
@@ -152,6 +178,11 @@ struct Halves {
     w1 = w[1];
     return at;
   }
+  // the half-tiles of range z of `ranges`
+  __device__ __forceinline__ int begin(int z, int ranges) const {
+    return (int)((int64_t)n * z / ranges);
+  }
+  __device__ __forceinline__ int end(int z, int ranges) const { return begin(z + 1, ranges); }
 };
 
 __device__ __forceinline__ bool on(uint32_t w0, uint32_t w1, int j) {
@@ -176,11 +207,11 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_fwd32(const xs::Params P
   for (int i = 0; i < 4; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
   }
+  clear<D>(acc);
   const float sl2 = P.scale * kLog2e;
-  for (int h = 0; h < H.n; ++h) {
+  const int h1 = H.end(blockIdx.z, P.nstate);
+  for (int h = H.begin(blockIdx.z, P.nstate); h < h1; ++h) {
     uint32_t w0, w1;
     const int64_t at = H.at(h, w0, w1);
     if (!(w0 | w1)) continue;
@@ -195,16 +226,16 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_fwd32(const xs::Params P
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = on(w0, w1, tx + 16 * j) ? s[i][j] * sl2 : -INFINITY;
+        s[i][j] = on(w0, w1, tx + 16 * j) ? s[i][j] : -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
-      const float mn = fmaxf(m[i], row_max(top));
+      const float mn = fmaxf(m[i], row_max(top) * sl2);
       const float base = mn == -INFINITY ? 0.f : mn;
       const float f = exp2f(m[i] - base);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = exp2f(s[i][j] - base);
+        const float p = exp2f(fmaf(s[i][j], sl2, -base));
         sum += p;
         sp[(4 * ty + i) * kP + tx + 16 * j] = p;
       }
@@ -221,10 +252,13 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_fwd32(const xs::Params P
     const int64_t row = row0 + 4 * ty + i;
     if (row >= P.np) continue;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    const bool parts = P.nstate > 1;
+    const int64_t at = (parts ? blockIdx.z * P.bh * P.np : 0) + bh * P.np + row;
+    float* const o = (parts ? P.part : P.out) + at * D;
+    float* const lse = parts ? P.part_lse : P.out_lse;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) P.out[(bh * P.np + row) * D + tx + 16 * c] = acc[i][c] * inv;
-    if (P.out_lse && tx == 0)
-      P.out_lse[bh * P.np + row] = l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
+    for (int c = 0; c < D / 16; ++c) o[tx + 16 * c] = acc[i][c] * inv;
+    if (lse && tx == 0) lse[at] = l[i] == 0.f ? -INFINITY : fmaf(m[i], kLn2, logf(l[i]));
   }
 }
 
@@ -260,7 +294,7 @@ __device__ __forceinline__ void grads(const float* sq, const float* sg, const fl
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool in = on(w0, w1, tx + 16 * j);
-      const float p = in ? exp2f(fmaf(s[i][j], scale * kLog2e, nl[i])) : 0.f;
+      const float p = in ? expf(fmaf(s[i][j], scale, nl[i])) : 0.f;
       const int at = (4 * ty + i) * kP + tx + 16 * j;
       if (sp) sp[at] = p;
       sd[at] = p * (g[i][j] - dl[i]) * scale;
@@ -288,12 +322,12 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_dq32(const xs::Params P)
     const int64_t row = row0 + 4 * ty + i;
     const bool in = row < P.np;
     const float lse = in ? P.lse[bh * P.np + row] : -INFINITY;
-    nl[i] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    nl[i] = lse == -INFINITY ? -INFINITY : -lse;  // a row without any state: p = 0
     dl[i] = in ? P.delta[bh * P.np + row] : 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
   }
-  for (int h = 0; h < H.n; ++h) {
+  clear<D>(acc);
+  const int h1 = H.end(blockIdx.z, P.nstate);
+  for (int h = H.begin(blockIdx.z, P.nstate); h < h1; ++h) {
     uint32_t w0, w1;
     const int64_t at = H.at(h, w0, w1);
     if (!(w0 | w1)) continue;
@@ -309,8 +343,10 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_dq32(const xs::Params P)
   for (int i = 0; i < 4; ++i) {
     const int64_t row = row0 + 4 * ty + i;
     if (row >= P.np) continue;
+    float* const dq = (P.nstate > 1 ? P.part + blockIdx.z * P.bh * P.np * D : P.out) +
+                      (bh * P.np + row) * D;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) P.out[(bh * P.np + row) * D + tx + 16 * c] = acc[i][c];
+    for (int c = 0; c < D / 16; ++c) dq[tx + 16 * c] = acc[i][c];
   }
 }
 
@@ -334,10 +370,8 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_dkv32(const xs::Params P
   load_tile<D>(sk, P.k + bh * P.l * D, at, P.l, w0, w1);
   load_tile<D>(sv, P.v + bh * P.l * D, at, P.l, w0, w1);
   float ak[4][D / 16], av[4][D / 16];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
+  clear<D>(ak);
+  clear<D>(av);
   const int64_t qt = (P.np + kT - 1) / kT;
   const int64_t t0 = qt * split / P.nsplit, t1 = (w0 | w1) ? qt * (split + 1) / P.nsplit : t0;
   for (int64_t t = t0; t < t1; ++t) {
@@ -351,7 +385,7 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_dkv32(const xs::Params P
       const int64_t row = row0 + 4 * ty + i;
       const bool in = row < P.np;
       const float lse = in ? P.lse[bh * P.np + row] : -INFINITY;
-      nl[i] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+      nl[i] = lse == -INFINITY ? -INFINITY : -lse;  // a row without any state: p = 0
       dl[i] = in ? P.delta[bh * P.np + row] : 0.f;
     }
     __syncthreads();
@@ -388,6 +422,20 @@ __global__ void __launch_bounds__(256)
   *reinterpret_cast<float4*>((blockIdx.y ? dv : dk) + i) = s;
 }
 
+// State ranges of o and dq: enough blocks for two per SM, at least two tiles of 64 states each.
+// (A single row over a long context would otherwise be the work of one block; more ranges than SMs
+// hold only add partial rows.)
+static int state_ranges(const Problem& p) {
+  const int64_t blocks = p.bh * ((p.np + xs::kT - 1) / xs::kT);
+  const int64_t most = (p.l + 2 * xs::kT - 1) / (2 * xs::kT);
+  int64_t n = 2 * (int64_t)sm_count() / blocks;
+  if (n > most) n = most;
+  return n < 1 ? 1 : (int)(n < kMaxSplits ? n : kMaxSplits);
+}
+static size_t part_bytes(const Problem& p, int n) {
+  return n > 1 ? align256((size_t)n * p.bh * p.np * p.d * sizeof(float)) : 0;
+}
+
 static xs::Params simt_params(const Problem& p, const MaskTables& m) {
   xs::Params P{};
   P.q = static_cast<const float*>(p.q);
@@ -401,6 +449,7 @@ static xs::Params simt_params(const Problem& p, const MaskTables& m) {
   P.words = m.words;
   P.tiles = m.tiles;
   P.kv_heads = p.kv_heads;
+  P.nstate = state_ranges(p);
   P.nsplit = 1;
   P.scale = p.scale;
   return P;
@@ -420,14 +469,24 @@ template <int D> static cudaError_t launch_fwd32(const Problem& p, xs::Params P)
   const cudaError_t e =
       smem_attr_once(reinterpret_cast<const void*>(k_cross_fwd32<D>), bytes, attr);
   if (e != cudaSuccess) return e;
-  k_cross_fwd32<D><<<dim3((unsigned)((p.np + xs::kT - 1) / xs::kT), (unsigned)p.bh), xs::kThreads,
-                     bytes, p.s>>>(P);
+  k_cross_fwd32<D><<<dim3((unsigned)((p.np + xs::kT - 1) / xs::kT), (unsigned)p.bh, P.nstate),
+                     xs::kThreads, bytes, p.s>>>(P);
   count_launch();
+  if (P.nstate > 1) return join_splits(p, P.part, P.part_lse, P.nstate, P.out, P.out_lse);
   return cudaGetLastError();
 }
 
-cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse) {
+size_t fwd_simt_bytes(const Problem& p) {
+  const int n = state_ranges(p);
+  return n > 1 ? part_bytes(p, n) + align256((size_t)n * p.bh * p.np * sizeof(float)) : 0;
+}
+
+cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse, void* ws) {
   xs::Params P = simt_params(p, m);
+  if (P.nstate > 1) {
+    P.part = static_cast<float*>(ws);
+    P.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part_bytes(p, P.nstate));
+  }
   P.out = static_cast<float*>(o);
   P.out_lse = lse;
   switch (p.d) {
@@ -440,7 +499,8 @@ cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse)
 
 size_t bwd_simt_bytes(const Problem& p) {
   const size_t n = dkv_splits(p), e = (size_t)p.bh * p.l * p.d * sizeof(float);
-  return align256((size_t)p.bh * p.np * sizeof(float)) + (n > 1 ? 2 * align256(n * e) : 0);
+  return align256((size_t)p.bh * p.np * sizeof(float)) + part_bytes(p, state_ranges(p)) +
+         (n > 1 ? 2 * align256(n * e) : 0);
 }
 
 template <int D> static cudaError_t launch_bwd32(const Problem& p, xs::Params P, float* dk, float* dv) {
@@ -452,8 +512,14 @@ template <int D> static cudaError_t launch_bwd32(const Problem& p, xs::Params P,
     e = smem_attr_once(reinterpret_cast<const void*>(k_cross_dkv32<D>), bk, ak);
   if (e != cudaSuccess) return e;
   k_cross_delta32<D><<<(unsigned)((p.bh * p.np + 31) / 32), 256, 0, p.s>>>(P);
-  k_cross_dq32<D><<<dim3((unsigned)((p.np + xs::kT - 1) / xs::kT), (unsigned)p.bh), xs::kThreads,
-                    bq, p.s>>>(P);
+  k_cross_dq32<D><<<dim3((unsigned)((p.np + xs::kT - 1) / xs::kT), (unsigned)p.bh, P.nstate),
+                    xs::kThreads, bq, p.s>>>(P);
+  if (P.nstate > 1) {
+    const int64_t n = p.bh * p.np * D;
+    k_cross_sum32<<<dim3((unsigned)((n / 4 + 255) / 256), 1), 256, 0, p.s>>>(
+        P.part, P.nstate, n, P.out, nullptr, nullptr);
+    count_launch();
+  }
   const int64_t halves = (p.l + xs::kT - 1) / xs::kT;
   k_cross_dkv32<D><<<dim3((unsigned)(halves * P.nsplit), (unsigned)p.bh), xs::kThreads, bk, p.s>>>(P);
   count_launch(3);
@@ -476,6 +542,8 @@ cudaError_t bwd_simt(const Problem& p, const MaskTables& m, const void* o, const
   uint8_t* at = static_cast<uint8_t*>(ws);
   P.delta = reinterpret_cast<float*>(at);
   at += align256((size_t)p.bh * p.np * sizeof(float));
+  P.part = reinterpret_cast<float*>(at);
+  at += part_bytes(p, P.nstate);
   P.nsplit = dkv_splits(p);
   P.dk = static_cast<float*>(dk);
   P.dv = static_cast<float*>(dv);

@@ -257,3 +257,20 @@ def test_wait_timeout_is_reported_and_the_next_call_is_right():
         assert m3.pack3d_read_status(status) == 0
     f2, g2 = run_and_check(q, k, v, m, dO)
     assert torch.equal(f["o"], f2["o"]) and torch.equal(g["dk"], g2["dk"])
+
+
+@pytest.mark.parametrize("d", [48, 64, 96, 128])
+@pytest.mark.parametrize("B,H,HK,N,L,mask", [
+    (1, 8, 2, 1, 5000, "none"), (2, 4, 4, 1, 4097, "pad"), (1, 2, 1, 3, 16384, "sparse"),
+    (3, 1, 1, 200, 2049, "random"), (2, 1, 1, 1, 300, "empty")])
+def test_few_rows_over_a_long_context_f32(d, B, H, HK, N, L, mask):
+    # ranges of states in blocks of their own: o and lse joined, dq summed
+    q, k, v, m, dO = make(B, H, HK, N, L, d, torch.float32, mask, seed=5, garbage=True)
+    f, g = run_and_check(q, k, v, m, dO)
+    again = p3d().pack3d_cross_attn_fwd(q, k, v, mask=m, save_for_backward=True)
+    assert torch.equal(f["o"], again["o"]) and torch.equal(f["lse"], again["lse"])
+    g2 = p3d().pack3d_cross_attn_bwd(q, k, v, f, dO, mask=m)
+    assert all(torch.equal(g[n], g2[n]) for n in ("dq", "dk", "dv"))
+    # without lse
+    o = p3d().pack3d_cross_attn_fwd(q, k, v, mask=m)["o"]
+    assert torch.equal(o, f["o"])
