@@ -4,14 +4,16 @@
 //   dq_i = sum_j dS_ij k_j,   dk_j = sum_i dS_ij q_i,   dv_j = sum_i p_ij dO_i.
 //
 //   k_cross_dq    row-major: a CTA walks 128-row tiles; first D of the tile's rows (left for
-//                 k_cross_dkv too); per 64 states S = q K^T and dP = dO V^T, dS in bf16, dq += dS K. Two CTAs per SM, so that one tile's products run
-//                 under the other's elementwise pass and epilogue.
+//                 k_cross_dkv too); per 64 states S = q K^T and dP = dO V^T, dS in bf16, dq += dS K.
+//                 Two CTAs per SM, so that one tile's products run under the other's elementwise
+//                 pass and epilogue. Few row tiles: the states in ranges, a unit each, whose fp32
+//                 sums k_cross_sum adds in order.
 //   k_cross_dkv   state-major: a CTA owns 128 states of one problem and a range of rows; per 64 rows
 //                 S^T = K q^T and dP^T = V dO^T (double-buffered in TMEM), P^T and dS^T in bf16 over
 //                 them, dv += P^T dO and dk += dS^T q. Two groups of elementwise warps take turns.
 //   k_cross_sum   the row ranges' partial dk, dv, added in range order (no atomics anywhere).
 // A KV head's gradients sum over its query heads, which are rows of the same problem.
-// P and dS are rounded to bf16 for the second products (relative 2^-9, as the outputs).
+// P and dS are rounded to bf16 for the second products (relative 2^-8, as the outputs).
 // Masked states: in k_cross_dq their dS is zero whatever S and dP hold, and their K rows (which may
 // hold NaN) are zeroed in shared memory; in k_cross_dkv each state is an output row of its own, so
 // the masked rows' sums are simply not written and zeros are.
@@ -49,6 +51,8 @@ struct Params {
   long long budget;
   int64_t np, npad, l, bh, units, words;
   int rtiles, tiles, kv_heads, nsplit;
+  int nstate;               // k_cross_dq: ranges of states
+  float* part_q;            // [nstate][bh][np][D] where there are several
   float scale, scale_log2;
   __nv_bfloat16 *dk, *dv;   // written when nsplit is 1
   float *part_k, *part_v;   // [nsplit][bh][l][D] otherwise
@@ -88,13 +92,19 @@ template <int D> struct Cols {
   static_assert(kO + D <= 256, "tensor memory");
 };
 
-// A unit's problem, first row and steps of 64 states (the batch entry's listed tiles, halved).
+// A unit's problem, first row and steps of 64 states (the batch entry's listed tiles, halved): its
+// range z of them, from step j0 on. Range 0 is empty only if all are.
 struct Unit {
   int64_t bh, row0;
-  int n;
+  int n, z, j0;
   const int32_t* list;
   const uint32_t* bits;
   __device__ __forceinline__ Unit(const xb::Params& P, int64_t u) {
+    z = j0 = 0;
+    if (P.nstate > 1) {
+      z = (int)(u % P.nstate);
+      u /= P.nstate;
+    }
     bh = u / P.rtiles;
     row0 = (u % P.rtiles) * kTile;
     const int64_t b = bh / P.kv_heads;
@@ -106,8 +116,13 @@ struct Unit {
       bits = P.bits + b * P.words;
       n = 2 * list[-1];
     }
+    if (P.nstate > 1) {
+      j0 = (int)(((int64_t)n * z + P.nstate - 1) / P.nstate);
+      n = (int)(((int64_t)n * (z + 1) + P.nstate - 1) / P.nstate) - j0;
+    }
   }
   __device__ __forceinline__ int64_t at(int j) const {
+    j += j0;
     return list ? (int64_t)list[j >> 1] * kTile + (j & 1) * xb::kHalf : (int64_t)j * xb::kHalf;
   }
   __device__ __forceinline__ void words(int64_t l, int j, uint32_t (&w)[2]) const {
@@ -193,7 +208,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
           }
           if (le != -INFINITY) rd = make_float2(-le * kLog2e, d * P.scale);
         }
-        P.rows[U.bh * P.npad + row] = rd;
+        if (U.z == 0) P.rows[U.bh * P.npad + row] = rd;
       }
       const float2 nl2 = make_float2(rd.x, rd.x), nd2 = make_float2(-rd.y, -rd.y);
       const float2 sl2 = make_float2(P.scale_log2, P.scale_log2);
@@ -250,7 +265,12 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
       if (U.n && !ab.all(sb + 8 * (B_DONE), (gc - 1) & 1)) break;
       if (!U.n) {
         // no state: zero rows
-        if (U.row0 + rin < P.np) {
+        if (U.row0 + rin < P.np && P.nstate > 1) {
+          float* dst = P.part_q + ((U.z * P.bh + U.bh) * P.np + U.row0 + rin) * D;
+#pragma unroll
+          for (int e = 0; e < D; e += 4)
+            *reinterpret_cast<float4*>(dst + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if (U.row0 + rin < P.np) {
           __nv_bfloat16* dst = P.dk + (U.bh * P.np + U.row0 + rin) * D;
 #pragma unroll
           for (int e = 0; e < D; e += 8)
@@ -264,6 +284,15 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
         uint32_t o[16];
         tc::tmem_ld16(tl + C::kO + c, o);
         tc::tmem_wait_ld();
+        if (P.nstate > 1) {
+          if (U.row0 + rin < P.np) {
+            float* dst = P.part_q + ((U.z * P.bh + U.bh) * P.np + U.row0 + rin) * D + c;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+          continue;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[4];
@@ -282,7 +311,7 @@ __global__ void __launch_bounds__(xq::kThreads, 2)
       if (rin == 0) {
         if (!ab.wait(sb + 8 * (B_STAGED), staged++ & 1)) ok = false;
 #pragma unroll
-        for (int c = 0; c < Ly::NB && ok; ++c)
+        for (int c = 0; c < Ly::NB && ok && P.nstate == 1; ++c)
           tma_store_3d(&mo, smem + S::kQ + c * kTile * Ly::RB, c * Ly::CW, (int)U.row0, (int)U.bh);
         bulk_commit();
         bulk_wait_read();
@@ -762,11 +791,28 @@ static int dkv_ranges(const Problem& p) {
   return best;
 }
 
+// State ranges of the row-major kernel (two CTAs per SM): only when the row tiles leave half of the SMs
+// without a CTA, at least four steps of 64 states each. (8 heads of one token over 16,384 states of 64:
+// training step 252 -> 92 us; two ranges of 16,000 rows over 1,000 states, whose partial rows are 8 MB,
+// took 86 us against 82.)
+static int dq_ranges(const Problem& p) {
+  const int64_t units = p.bh * ((p.np + kTile - 1) / kTile);
+  const int64_t steps = (p.l + xb::kHalf - 1) / xb::kHalf;
+  int64_t n = 2 * (int64_t)sm_count() / units;
+  if (n > steps / 4) n = steps / 4;
+  return n < 4 ? 1 : (int)n;
+}
+static size_t dq_part_bytes(const Problem& p) {
+  const int n = dq_ranges(p);
+  return n > 1 ? align256((size_t)n * p.bh * p.np * p.d * sizeof(float)) : 0;
+}
+
 size_t bwd_tc_bytes(const Problem& p) {
   const int64_t npad = (p.np + kTile - 1) / kTile * kTile;
   const int n = dkv_ranges(p);
   const size_t e = (size_t)n * p.bh * p.l * p.d * sizeof(float);
-  return align256((size_t)p.bh * npad * sizeof(float2)) + (n > 1 ? 2 * align256(e) : 0);
+  return align256((size_t)p.bh * npad * sizeof(float2)) + dq_part_bytes(p) +
+         (n > 1 ? 2 * align256(e) : 0);
 }
 
 template <int D>
@@ -821,17 +867,26 @@ static cudaError_t launch_bwd(const Problem& p, const MaskTables& m, const void*
   P.scale_log2 = p.scale * kLog2e;
   // dq: persistent, two CTAs per SM
   P.nsplit = 1;
-  P.units = p.bh * P.rtiles;
+  P.nstate = dq_ranges(p);
+  P.units = p.bh * P.rtiles * P.nstate;
+  uint8_t* at = static_cast<uint8_t*>(ws) + align256((size_t)p.bh * npad * sizeof(float2));
+  P.part_q = reinterpret_cast<float*>(at);
+  at += dq_part_bytes(p);
   P.dk = static_cast<__nv_bfloat16*>(dq);
   const int64_t cap = 2 * (int64_t)sm_count();
   k_cross_dq<D><<<(unsigned)(P.units < cap ? P.units : cap), xq::kThreads, Sq::kBytes, p.s>>>(
       q128, g128, k64, v64, o128, P);
+  if (P.nstate > 1) {
+    const int64_t n = p.bh * p.np * D;
+    k_cross_sum<<<dim3((unsigned)((n / 4 + 255) / 256), 1), 256, 0, p.s>>>(
+        P.part_q, nullptr, P.nstate, n, P.dk, nullptr);
+    count_launch();
+  }
   // dk, dv
   P.nsplit = dkv_ranges(p);
   P.dk = static_cast<__nv_bfloat16*>(dk);
   P.dv = static_cast<__nv_bfloat16*>(dv);
   if (P.nsplit > 1) {
-    uint8_t* at = static_cast<uint8_t*>(ws) + align256((size_t)p.bh * npad * sizeof(float2));
     P.part_k = reinterpret_cast<float*>(at);
     P.part_v = reinterpret_cast<float*>(
         at + align256((size_t)P.nsplit * p.bh * p.l * D * sizeof(float)));

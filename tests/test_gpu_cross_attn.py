@@ -274,3 +274,15 @@ def test_few_rows_over_a_long_context_f32(d, B, H, HK, N, L, mask):
     # without lse
     o = p3d().pack3d_cross_attn_fwd(q, k, v, mask=m)["o"]
     assert torch.equal(o, f["o"])
+
+
+@pytest.mark.parametrize("d", [48, 64, 96, 128])
+@pytest.mark.parametrize("B,H,HK,N,L,mask", [
+    (1, 2, 2, 1, 6000, "none"), (3, 4, 2, 130, 4099, "pad"), (2, 2, 1, 200, 2049, "empty"),
+    (2, 3, 3, 1, 8192, "sparse"), (1, 2, 2, 300, 1100, "left")])
+def test_gradients_of_few_rows_over_a_long_context(d, B, H, HK, N, L, mask):
+    # the rows' gradients summed over ranges of states, some of them without a step
+    q, k, v, m, dO = make(B, H, HK, N, L, d, torch.bfloat16, mask, seed=17, garbage=True)
+    f, g = run_and_check(q, k, v, m, dO)
+    g2 = p3d().pack3d_cross_attn_bwd(q, k, v, f, dO, mask=m)
+    assert all(torch.equal(g[n], g2[n]) for n in ("dq", "dk", "dv"))
