@@ -16,6 +16,8 @@
 // term would move a whole row's probabilities.
 #include <math.h>
 
+#include <algorithm>
+
 #include "cross.h"
 #include "launch.h"
 
@@ -70,6 +72,25 @@ __device__ __forceinline__ void product(const float* a, const float* b, int ty, 
   }
 }
 
+// The D / 16 columns of thread tx: pairs of neighbours (one 8-byte load from shared memory feeds
+// eight FMAs; single columns would take as many load cycles as FMAs), and one more where D is an odd
+// number of sixteens.
+template <int D> __device__ __forceinline__ void columns(const float* row, int tx, float (&y)[D / 16]) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    const float2 x = *reinterpret_cast<const float2*>(row + 32 * c + 2 * tx);
+    y[2 * c] = x.x;
+    y[2 * c + 1] = x.y;
+  }
+  if (D % 32) y[D / 16 - 1] = row[D / 32 * 32 + tx];
+}
+template <int D>
+__device__ __forceinline__ void store_columns(float* row, int tx, const float (&y)[D / 16], float f) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+    *reinterpret_cast<float2*>(row + 32 * c + 2 * tx) = make_float2(y[2 * c] * f, y[2 * c + 1] * f);
+  if (D % 32) row[D / 32 * 32 + tx] = y[D / 16 - 1] * f;
+}
 template <int D> __device__ __forceinline__ void clear(float (&a)[4][D / 16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -84,7 +105,7 @@ __device__ __forceinline__ void add(float (&acc)[4][D / 16], const float (&a)[4]
     for (int c = 0; c < D / 16; ++c) acc[i][c] += a[i][c];
 }
 
-// acc[i][c] += sum over the 64 inner rows of m[4 ty + i][inner] b[inner][tx + 16 c]
+// out[i][c] += sum over the 64 inner rows of m[4 ty + i][inner] b[inner][column c of tx]
 template <int D>
 __device__ __forceinline__ void accumulate(const float* m, const float* b, int ty, int tx,
                                            float (&out)[4][D / 16]) {
@@ -97,35 +118,36 @@ __device__ __forceinline__ void accumulate(const float* m, const float* b, int t
     for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(m + (4 * ty + i) * kP + k);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      float y[D / 16];
+      columns<D>(b + (k + e) * pitch<D>(), tx, y);
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const float y = b[(k + e) * pitch<D>() + tx + 16 * c];
+      for (int c = 0; c < D / 16; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          acc[i][c] = fmaf(e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w, y,
+          acc[i][c] = fmaf(e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w, y[c],
                            acc[i][c]);
-      }
     }
   }
   add<D>(out, acc);
 }
 
-// As accumulate with m transposed: acc[i][c] += sum over rows r of m[r][4 ty + i] b[r][tx + 16 c]
+// As accumulate with m transposed: out[i][c] += sum over rows r < n of m[r][4 ty + i] b[r][column c]
 template <int D>
-__device__ __forceinline__ void accumulate_t(const float* m, const float* b, int ty, int tx,
+__device__ __forceinline__ void accumulate_t(const float* m, const float* b, int n, int ty, int tx,
                                              float (&out)[4][D / 16]) {
   float acc[4][D / 16];
   clear<D>(acc);
 #pragma unroll 4
-  for (int r = 0; r < kT; ++r) {
+  for (int r = 0; r < n; ++r) {
     const float4 x = *reinterpret_cast<const float4*>(m + r * kP + 4 * ty);
+    float y[D / 16];
+    columns<D>(b + r * pitch<D>(), tx, y);
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
-      const float y = b[r * pitch<D>() + tx + 16 * c];
-      acc[0][c] = fmaf(x.x, y, acc[0][c]);
-      acc[1][c] = fmaf(x.y, y, acc[1][c]);
-      acc[2][c] = fmaf(x.z, y, acc[2][c]);
-      acc[3][c] = fmaf(x.w, y, acc[3][c]);
+      acc[0][c] = fmaf(x.x, y[c], acc[0][c]);
+      acc[1][c] = fmaf(x.y, y[c], acc[1][c]);
+      acc[2][c] = fmaf(x.z, y[c], acc[2][c]);
+      acc[3][c] = fmaf(x.w, y[c], acc[3][c]);
     }
   }
   add<D>(out, acc);
@@ -185,13 +207,17 @@ struct Halves {
   __device__ __forceinline__ int end(int z, int ranges) const { return begin(z + 1, ranges); }
 };
 
+// Whether the warp's 8 rows of a tile hold one of the problem's: a few rows are the work of a few warps.
+__device__ __forceinline__ bool warp_lives(int64_t row0, int64_t np) {
+  return row0 + (threadIdx.x >> 5) * 8 < np;
+}
 __device__ __forceinline__ bool on(uint32_t w0, uint32_t w1, int j) {
   return ((j < 32 ? w0 : w1) >> (j & 31)) & 1u;
 }
 }  // namespace xs
 
 template <int D>
-__global__ void __launch_bounds__(xs::kThreads) k_cross_fwd32(const xs::Params P) {
+__global__ void __launch_bounds__(xs::kThreads, D <= 96 ? 2 : 1) k_cross_fwd32(const xs::Params P) {
   using namespace xs;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;
@@ -200,6 +226,7 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_fwd32(const xs::Params P
   float* sp = sv + kT * pitch<D>();
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int64_t bh = blockIdx.y, row0 = (int64_t)blockIdx.x * kT;
+  const bool live = warp_lives(row0, P.np);
   const Halves H(P, bh);
   load_tile<D>(sq, P.q + bh * P.np * D, row0, P.np, ~0u, ~0u);
   float acc[4][D / 16], m[4], l[4];
@@ -219,6 +246,7 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_fwd32(const xs::Params P
     load_tile<D>(sk, P.k + bh * P.l * D, at, P.l, w0, w1);
     load_tile<D>(sv, P.v + bh * P.l * D, at, P.l, w0, w1);
     __syncthreads();
+    if (!live) continue;
     float s[4][4];
     product<D>(sq, sk, ty, tx, s);
 #pragma unroll
@@ -256,8 +284,7 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_fwd32(const xs::Params P
     const int64_t at = (parts ? blockIdx.z * P.bh * P.np : 0) + bh * P.np + row;
     float* const o = (parts ? P.part : P.out) + at * D;
     float* const lse = parts ? P.part_lse : P.out_lse;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) o[tx + 16 * c] = acc[i][c] * inv;
+    store_columns<D>(o, tx, acc[i], inv);
     if (lse && tx == 0) lse[at] = l[i] == 0.f ? -INFINITY : fmaf(m[i], kLn2, logf(l[i]));
   }
 }
@@ -280,15 +307,19 @@ __global__ void __launch_bounds__(256) k_cross_delta32(const xs::Params P) {
 }
 
 namespace xs {
-// Scores of a tile as probabilities (into sp, if any) and dS (into sd).
-template <int D>
+// Scores of a tile as probabilities (into sp, if any) and dS (into sd, which may lie over sv: `over`).
+template <int D, bool over>
 __device__ __forceinline__ void grads(const float* sq, const float* sg, const float* sk,
                                       const float* sv, float* sp, float* sd, int ty, int tx,
                                       const float (&nl)[4], const float (&dl)[4], uint32_t w0,
-                                      uint32_t w1, float scale) {
+                                      uint32_t w1, float scale, bool live) {
   float s[4][4], g[4][4];
-  product<D>(sq, sk, ty, tx, s);
-  product<D>(sg, sv, ty, tx, g);
+  if (live) {
+    product<D>(sq, sk, ty, tx, s);
+    product<D>(sg, sv, ty, tx, g);
+  }
+  if (over) __syncthreads();  // V has been read
+  if (!live) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -303,16 +334,17 @@ __device__ __forceinline__ void grads(const float* sq, const float* sg, const fl
 }  // namespace xs
 
 template <int D>
-__global__ void __launch_bounds__(xs::kThreads) k_cross_dq32(const xs::Params P) {
+__global__ void __launch_bounds__(xs::kThreads, D <= 96 ? 2 : 1) k_cross_dq32(const xs::Params P) {
   using namespace xs;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;
   float* sg = sq + kT * pitch<D>();
   float* sk = sg + kT * pitch<D>();
   float* sv = sk + kT * pitch<D>();
-  float* sd = sv + kT * pitch<D>();
+  float* sd = sv;  // dS over V, so that two blocks share an SM up to d = 96
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int64_t bh = blockIdx.y, row0 = (int64_t)blockIdx.x * kT;
+  const bool live = warp_lives(row0, P.np);
   const Halves H(P, bh);
   load_tile<D>(sq, P.q + bh * P.np * D, row0, P.np, ~0u, ~0u);
   load_tile<D>(sg, P.dO + bh * P.np * D, row0, P.np, ~0u, ~0u);
@@ -335,9 +367,9 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_dq32(const xs::Params P)
     load_tile<D>(sk, P.k + bh * P.l * D, at, P.l, w0, w1);
     load_tile<D>(sv, P.v + bh * P.l * D, at, P.l, w0, w1);
     __syncthreads();
-    grads<D>(sq, sg, sk, sv, nullptr, sd, ty, tx, nl, dl, w0, w1, P.scale);
+    grads<D, true>(sq, sg, sk, sv, nullptr, sd, ty, tx, nl, dl, w0, w1, P.scale, live);
     __syncwarp();
-    accumulate<D>(sd, sk, ty, tx, acc);
+    if (live) accumulate<D>(sd, sk, ty, tx, acc);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -345,13 +377,12 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_dq32(const xs::Params P)
     if (row >= P.np) continue;
     float* const dq = (P.nstate > 1 ? P.part + blockIdx.z * P.bh * P.np * D : P.out) +
                       (bh * P.np + row) * D;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) dq[tx + 16 * c] = acc[i][c];
+    store_columns<D>(dq, tx, acc[i], 1.f);
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(xs::kThreads) k_cross_dkv32(const xs::Params P) {
+__global__ void __launch_bounds__(xs::kThreads, D <= 64 ? 2 : 1) k_cross_dkv32(const xs::Params P) {
   using namespace xs;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;
@@ -389,21 +420,20 @@ __global__ void __launch_bounds__(xs::kThreads) k_cross_dkv32(const xs::Params P
       dl[i] = in ? P.delta[bh * P.np + row] : 0.f;
     }
     __syncthreads();
-    grads<D>(sq, sg, sk, sv, sp, sd, ty, tx, nl, dl, w0, w1, P.scale);
+    grads<D, false>(sq, sg, sk, sv, sp, sd, ty, tx, nl, dl, w0, w1, P.scale,
+                    warp_lives(row0, P.np));
     __syncthreads();
-    accumulate_t<D>(sp, sg, ty, tx, av);
-    accumulate_t<D>(sd, sq, ty, tx, ak);
+    const int n = P.np - row0 < kT ? (int)(P.np - row0 + 7) & ~7 : kT;  // rows of warps that live
+    accumulate_t<D>(sp, sg, n, ty, tx, av);
+    accumulate_t<D>(sd, sq, n, ty, tx, ak);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t row = at + 4 * ty + i;
     if (row >= P.l) continue;
     const int64_t dst = ((split * P.bh + bh) * P.l + row) * D;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      P.dk[dst + tx + 16 * c] = ak[i][c];
-      P.dv[dst + tx + 16 * c] = av[i][c];
-    }
+    store_columns<D>(P.dk + dst, tx, ak[i], 1.f);
+    store_columns<D>(P.dv + dst, tx, av[i], 1.f);
   }
 }
 
@@ -422,15 +452,32 @@ __global__ void __launch_bounds__(256)
   *reinterpret_cast<float4*>((blockIdx.y ? dv : dk) + i) = s;
 }
 
-// State ranges of o and dq: enough blocks for two per SM, at least two tiles of 64 states each.
-// (A single row over a long context would otherwise be the work of one block; more ranges than SMs
-// hold only add partial rows.)
+// Ranges that `items` blocks of `steps` tiles each are cut into: the count whose blocks fill the last
+// wave of `slots` best, at least 5 % better than fewer (partial rows are written and read again); a
+// block's fixed cost is about that of one tile. (A single row over a long context would otherwise be
+// the work of one block per problem: 8 heads over 16,384 states of 64, forward 660 -> 83 us; 160
+// blocks on 148 SMs would take two waves.)
+static int ranges(int64_t items, int64_t steps, int64_t slots) {
+  const int64_t most = std::min<int64_t>((4 * slots + items - 1) / items, kMaxSplits);
+  int best = 1;
+  double eff = 0.0;
+  for (int64_t n = 1; n <= most && n <= steps; ++n) {
+    const int64_t waves = (items * n + slots - 1) / slots;
+    const double e = (double)steps * items / (waves * slots * ((double)((steps + n - 1) / n) + 1.0));
+    if (e > eff * 1.05) {
+      eff = e;
+      best = (int)n;
+    }
+  }
+  return best;
+}
+static int64_t tiles64(int64_t n) { return (n + xs::kT - 1) / xs::kT; }
+// Ranges of states for o and dq (two blocks per SM up to d = 96), of rows for dk and dv (two up to 64).
 static int state_ranges(const Problem& p) {
-  const int64_t blocks = p.bh * ((p.np + xs::kT - 1) / xs::kT);
-  const int64_t most = (p.l + 2 * xs::kT - 1) / (2 * xs::kT);
-  int64_t n = 2 * (int64_t)sm_count() / blocks;
-  if (n > most) n = most;
-  return n < 1 ? 1 : (int)(n < kMaxSplits ? n : kMaxSplits);
+  return ranges(p.bh * tiles64(p.np), tiles64(p.l), (p.d <= 96 ? 2 : 1) * (int64_t)sm_count());
+}
+static int row_ranges(const Problem& p) {
+  return ranges(p.bh * tiles64(p.l), tiles64(p.np), (p.d <= 64 ? 2 : 1) * (int64_t)sm_count());
 }
 static size_t part_bytes(const Problem& p, int n) {
   return n > 1 ? align256((size_t)n * p.bh * p.np * p.d * sizeof(float)) : 0;
@@ -453,14 +500,6 @@ static xs::Params simt_params(const Problem& p, const MaskTables& m) {
   P.nsplit = 1;
   P.scale = p.scale;
   return P;
-}
-
-// Row ranges of the key gradients: enough blocks for two per SM.
-static int dkv_splits(const Problem& p) {
-  const int64_t blocks = p.bh * ((p.l + xs::kT - 1) / xs::kT), qt = (p.np + xs::kT - 1) / xs::kT;
-  int64_t n = (2 * (int64_t)sm_count() + blocks - 1) / (blocks > 0 ? blocks : 1);
-  if (n > qt) n = qt;
-  return n < 1 ? 1 : (int)n;
 }
 
 template <int D> static cudaError_t launch_fwd32(const Problem& p, xs::Params P) {
@@ -498,14 +537,15 @@ cudaError_t fwd_simt(const Problem& p, const MaskTables& m, void* o, float* lse,
 }
 
 size_t bwd_simt_bytes(const Problem& p) {
-  const size_t n = dkv_splits(p), e = (size_t)p.bh * p.l * p.d * sizeof(float);
+  const size_t n = row_ranges(p), e = (size_t)p.bh * p.l * p.d * sizeof(float);
   return align256((size_t)p.bh * p.np * sizeof(float)) + part_bytes(p, state_ranges(p)) +
          (n > 1 ? 2 * align256(n * e) : 0);
 }
 
 template <int D> static cudaError_t launch_bwd32(const Problem& p, xs::Params P, float* dk, float* dv) {
   constexpr int tile = xs::kT * xs::pitch<D>();
-  constexpr int bq = 4 * (4 * tile + xs::kT * xs::kP), bk = bq + 4 * xs::kT * xs::kP;
+  constexpr int score = xs::kT * xs::kP;
+  constexpr int bq = 4 * (3 * tile + (tile > score ? tile : score)), bk = 4 * (4 * tile + 2 * score);
   static std::atomic<uint64_t> aq{0}, ak{0};
   cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(k_cross_dq32<D>), bq, aq);
   if (e == cudaSuccess)
@@ -544,7 +584,7 @@ cudaError_t bwd_simt(const Problem& p, const MaskTables& m, const void* o, const
   at += align256((size_t)p.bh * p.np * sizeof(float));
   P.part = reinterpret_cast<float*>(at);
   at += part_bytes(p, P.nstate);
-  P.nsplit = dkv_splits(p);
+  P.nsplit = row_ranges(p);
   P.dk = static_cast<float*>(dk);
   P.dv = static_cast<float*>(dv);
   if (P.nsplit > 1) {
