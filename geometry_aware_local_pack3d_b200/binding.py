@@ -409,7 +409,11 @@ def _here(t):
 
 def _stream_of(index, stream):
     """The CUDA stream handle the call runs on: `stream`, or the current one of device `index`."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, expected cuda:{index}")
+    return stream.cuda_stream
 
 
 def _new(stream, like, shape, dtype):

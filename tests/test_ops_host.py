@@ -171,3 +171,20 @@ def test_an_oracle_with_a_mistake_is_noticed():
     bad = ob.cross(q, k, v, torch.ones_like(mask))["o"][0]
     with pytest.raises(AssertionError):
         ob.check(bad, good, "o")
+
+
+def test_f32_cross_workspace_of_split_states_and_rows():
+    f = b.pack3d_cross_attn_workspace_bytes
+    # few rows over a long context: partial o and lse, partial dq, in 32 bits
+    assert f(0, 1, 2, 2, 1, 8192, 96) >= 2 * 2 * (96 + 1) * 4
+    assert f(0, 1, 2, 2, 1, 8192, 96, False, True) >= 2 * 4 + 2 * 2 * 96 * 4
+    # rows enough for every SM: none
+    assert f(0, 8, 8, 8, 65536, 300, 96) == 0
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 7
+    assert b._stream_of(1, Stream) == 7
+    with pytest.raises(ValueError):
+        b._stream_of(0, Stream)
