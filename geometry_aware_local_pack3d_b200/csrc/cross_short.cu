@@ -40,6 +40,7 @@ struct Params {
   int64_t np;
   int l, lp;             // states; rounded up to a multiple of 32
   int bh, tiles, kv_heads;
+  int bufs;              // backward: buffers of P and dS
   int per, more;         // units of a CTA: per, or one more for the first `more`
   float scale, scale_log2;
 };
@@ -342,13 +343,17 @@ namespace shb {
 constexpr int kThreads = 320;  // elementwise 0-3, row data and dq 4-7, TMA 8, MMA 9
 // P and dS come first: as M = 128 operands of fewer than 128 states they reach past their tiles,
 // into the operands behind them (rows of dk, dv that no state owns and nobody reads)
-template <int D> constexpr int bytes(int lp) {
-  return 2 * Lay<64>::RB * kTile * (lp / 32) + 2 * Lay<D>::bytes(lp) + 4 * Lay<D>::bytes(kTile) +
-         2 * kTile * 8 + 512 + 1024;
+template <int D> constexpr int bytes(int lp, int bufs) {
+  return bufs * 2 * Lay<64>::RB * kTile * (lp / 32) + 2 * Lay<D>::bytes(lp) +
+         5 * Lay<D>::bytes(kTile) + 2 * kTile * 8 + 512;
 }
+// Buffers of P and dS: two where they fit, so that a tile's elementwise pass runs under the products
+// of the one before (65,536 rows x 8 heads to 77 states of 48: @@).
+template <int D> constexpr int buffers(int lp) { return bytes<D>(lp, 2) <= sh::kSmem ? 2 : 1; }
 enum {
-  B_Q = 0, B_KV = 2, B_KREADY, B_S, B_SFREE, B_ROWS, B_PD = B_ROWS + 2, B_MM, B_DQFREE,
-  B_FLUSH, B_STAGED, B_DRAIN, B_COUNT
+  B_Q = 0, B_KV = 2, B_KREADY, B_S, B_SFREE, B_ROWS, B_PD = B_ROWS + 2, B_MM = B_PD + 2,
+  B_DQFREE = B_MM + 2,
+  B_FLUSH, B_STAGED, B_STFREE, B_DRAIN, B_COUNT
 };
 }  // namespace shb
 
@@ -361,17 +366,17 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
   using Ly = Lay<D>;
   using Lp = Lay<64>;  // P and dS: blocks of 32 states
   constexpr int QB = Ly::bytes(kTile);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int KB = Ly::bytes(P.lp), PB = kTile * P.lp * 2;
-  uint8_t* const sp = smem;
+  const int bufs = P.bufs;
+  uint8_t* const sp = smem;             // [buffers] P and dS
   uint8_t* const sd = sp + PB;
-  uint8_t* const sq = sd + PB;          // [2 buffers] q, [2] dO
+  uint8_t* const sq = sp + bufs * 2 * PB;  // [2 buffers] q, [2] dO
   uint8_t* const sg = sq + 2 * QB;
   uint8_t* const sk = sg + 2 * QB;
   uint8_t* const sv = sk + KB;
-  float2* const srow = reinterpret_cast<float2*>(sv + KB);  // [2][128] (-lse log2(e), D tau)
+  uint8_t* const so = sv + KB;          // dq rows on their way out
+  float2* const srow = reinterpret_cast<float2*>(so + QB);  // [2][128] (-lse log2(e), D tau)
   uint64_t* bars = reinterpret_cast<uint64_t*>(srow + 2 * kTile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + B_COUNT + 1);
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i)
       tc::mbar_init(&bars[i], i == B_KREADY || i == B_SFREE || i == B_ROWS || i == B_ROWS + 1 ||
-                                      i == B_PD || i == B_DQFREE || i == B_FLUSH || i == B_STAGED
+                                      i == B_PD || i == B_PD + 1 || i == B_DQFREE || i == B_FLUSH || i == B_STAGED
                                   ? 128
                                   : 1);
     abort_flag[0] = 0;
@@ -415,8 +420,10 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
         arrive32(sb + 8 * B_KREADY);
       }
       ok = ab.all(sb + 8 * (B_ROWS + (n & 1)), n >> 1) && ab.all(sb + 8 * B_S, n);
-      // P and dS are the previous tile's until its products have completed
-      if (n) ok = ok && ab.all(sb + 8 * B_MM, n - 1);
+      // P and dS are the tile's before (or the one before that) until its products have completed
+      if (n >= (uint32_t)bufs)
+        ok = ok && ab.all(sb + 8 * (B_MM + ((n - bufs) & 1)), (n - bufs) >> 1);
+      const int buf = bufs == 2 ? (n & 1) * 2 * PB : 0;
       if (!ok) break;
       tc::tc_fence_after();
       const float2 rd = srow[(n & 1) * kTile + rin];
@@ -451,7 +458,7 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
             pp[i] = tc::pack_bf16(p.x, p.y);
             pd[i] = tc::pack_bf16(p.x * t.x, p.y * t.y);
           }
-          const int at = Lp::piece(kTile, rin, 4 * h + q);
+          const int at = buf + Lp::piece(kTile, rin, 4 * h + q);
           *reinterpret_cast<uint4*>(sp + at) = make_uint4(pp[0], pp[1], pp[2], pp[3]);
           *reinterpret_cast<uint4*>(sd + at) = make_uint4(pd[0], pd[1], pd[2], pd[3]);
         }
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
       tc::tc_fence_before();
       tc::fence_proxy_async_smem();
       arrive32(sb + 8 * B_SFREE);
-      arrive32(sb + 8 * B_PD);
+      arrive32(sb + 8 * (B_PD + (n & 1)));
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ row data, dq, dk and dv
@@ -467,18 +474,30 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
     const uint32_t tl = tbase + ((uint32_t)((warp - 4) * 32) << 16);
     sh::Run ahead(P);
     bool ok = true;
+    // the o row and lse of unit `ahead`: asked for a unit before they are used, since a trip to HBM
+    // per tile in this chain took as long as the tile (144 us of the training step below)
+    uint4 orow[D / 8];
+    float le = -INFINITY;
+    auto fetch = [&]() {
+      const int64_t row = (int64_t)ahead.tile * kTile + rin, at = ahead.bh * P.np + row;
+      const bool in = ahead.left > 0 && row < P.np;
+      le = in ? P.lse[at] : -INFINITY;
+#pragma unroll
+      for (int pc = 0; pc < D / 8; ++pc)
+        orow[pc] = in ? *reinterpret_cast<const uint4*>(P.o + at * D + pc * 8)
+                      : make_uint4(0u, 0u, 0u, 0u);
+    };
+    fetch();
     // D = <dO, o> and lse of the rows of unit i
     auto rows = [&](uint32_t i) -> bool {
       if (!ab.all(sb + 8 * (B_Q + (i & 1)), i >> 1)) return false;
       const int64_t row = (int64_t)ahead.tile * kTile + rin;
-      float s = 0.f, le = -INFINITY;
+      float s = 0.f;
       if (row < P.np) {
-        const int64_t at = ahead.bh * P.np + row;
-        le = P.lse[at];
-#pragma unroll 2
+#pragma unroll
         for (int pc = 0; pc < D / 8; ++pc) {
           float a[8], b[8];
-          Vec<__nv_bfloat16>::load(P.o + at * D + pc * 8, a);
+          Vec<__nv_bfloat16>::unpack(orow[pc], a);
           Vec<__nv_bfloat16>::load_shared(
               reinterpret_cast<const __nv_bfloat16*>(sg + (i & 1) * QB + Ly::piece(kTile, rin, pc)),
               b);
@@ -491,6 +510,7 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
           make_float2(le == -INFINITY ? -INFINITY : -le * kLog2e, s * P.scale);
       arrive32(sb + 8 * (B_ROWS + (i & 1)));
       ahead.next(P);
+      fetch();
       return true;
     };
     ok = rows(0);
@@ -499,10 +519,11 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
     for (sh::Run R(P); R.left > 0 && ok; R.next(P), ++n) {
       // the next unit's rows while this one's products are under way
       if (ahead.left > 0) ok = rows(n + 1);
-      ok = ok && ab.all(sb + 8 * B_MM, n);
+      ok = ok && ab.all(sb + 8 * (B_MM + (n & 1)), n >> 1);
       if (!ok) break;
       tc::tc_fence_after();
-      // the tile's q rows have been consumed: their buffer takes the gradient's rows
+      if (n) ok = ab.all(sb + 8 * B_STFREE, n - 1);
+      if (!ok) break;
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
@@ -515,7 +536,7 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
           for (int i = 0; i < 4; ++i)
             pk[i] = tc::pack_bf16(__uint_as_float(o[8 * h + 2 * i]),
                                   __uint_as_float(o[8 * h + 2 * i + 1]));
-          *reinterpret_cast<uint4*>(sq + (n & 1) * QB + Ly::piece(kTile, rin, c / 8 + h)) =
+          *reinterpret_cast<uint4*>(so + Ly::piece(kTile, rin, c / 8 + h)) =
               make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
       }
@@ -564,15 +585,18 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
       uint32_t n = 0;
 #pragma unroll 1
       for (sh::Run R(P); R.left > 0; R.next(P), ++n) {
+        // the next rows as soon as the products that read their buffers have completed
+        if (ahead.left > 0) {
+          if (!ab.wait(sb + 8 * (B_MM + (n & 1)), n >> 1)) break;
+          load();
+        }
         if (!ab.wait(sb + 8 * B_STAGED, n)) break;
 #pragma unroll 1
         for (int c = 0; c < Ly::NB; ++c)
-          tma_store_3d(&mo, sq + (n & 1) * QB + c * kTile * Ly::RB, c * Ly::CW, R.tile * kTile,
-                       R.bh);
+          tma_store_3d(&mo, so + c * kTile * Ly::RB, c * Ly::CW, R.tile * kTile, R.bh);
         bulk_commit();
         bulk_wait_read();
-        // (the products that read the buffers' rows completed before the gradient was staged)
-        if (ahead.left > 0) load();
+        arrive32(sb + 8 * B_STFREE);
       }
       bulk_wait();
       // an aborted run leaves no copy in flight
@@ -617,7 +641,9 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
         // the unit's scores have not been formed ahead
         if (R.fresh) {
           // the products before have read K and V, and their dk, dv have been taken out
-          if (n) ok = ab.all(sb + 8 * B_MM, n - 1) && ab.all(sb + 8 * B_FLUSH, gen - 1);
+          if (n)
+            ok = ab.all(sb + 8 * (B_MM + ((n - 1) & 1)), (n - 1) >> 1) &&
+                 ab.all(sb + 8 * B_FLUSH, gen - 1);
           if (!ok) break;
           if (lane == 0) {
             tc::mbar_expect_tx(&bars[B_KV], 2 * KB);
@@ -644,23 +670,24 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
         ++issued;
         ahead.next(P);
       }
-      ok = ab.all(sb + 8 * B_PD, n) && (n == 0 || ab.all(sb + 8 * B_DQFREE, n - 1));
+      ok = ab.all(sb + 8 * (B_PD + (n & 1)), n >> 1) && (n == 0 || ab.all(sb + 8 * B_DQFREE, n - 1));
       if (!ok) break;
       tc::tc_fence_after();
       if (tc::elect_one()) {
         const uint64_t bo = (uint64_t)(((n & 1) * QB) >> 4);
+        const uint64_t po = bufs == 2 ? (uint64_t)(((n & 1) * 2 * PB) >> 4) : 0;
         const uint32_t more = R.fresh ? 0u : 1u;
 #pragma unroll 1
         for (int ks = 0; ks < P.lp / 16; ++ks)
-          tc::mma_ss(tb + cQ, dk + sh::koff<64>(kTile, ks), km + Ly::moff(ks),
+          tc::mma_ss(tb + cQ, dk + po + sh::koff<64>(kTile, ks), km + Ly::moff(ks),
                      id_q, ks > 0);
 #pragma unroll 1
         for (int ks = 0; ks < kTile / 16; ++ks) {
           const uint32_t acc = ks > 0 ? 1u : more;
-          tc::mma_ss(tb + cV, pm + Lp::moff(ks), gm0 + bo + Ly::moff(ks), id_k, acc);
-          tc::mma_ss(tb + cK, dm + Lp::moff(ks), qm0 + bo + Ly::moff(ks), id_k, acc);
+          tc::mma_ss(tb + cV, pm + po + Lp::moff(ks), gm0 + bo + Ly::moff(ks), id_k, acc);
+          tc::mma_ss(tb + cK, dm + po + Lp::moff(ks), qm0 + bo + Ly::moff(ks), id_k, acc);
         }
-        commit32(sb + 8 * B_MM);
+        commit32(sb + 8 * (B_MM + (n & 1)));
       }
       __syncwarp();
     }
@@ -790,9 +817,10 @@ static cudaError_t launch_bwd_short(const Problem& p, const void* o, const float
     return cudaErrorInvalidValue;
   P.o = static_cast<const __nv_bfloat16*>(o);
   P.lse = lse;
+  P.bufs = shb::buffers<D>(P.lp);
   P.part_k = static_cast<float*>(ws);
   P.part_v = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + bwd_short_bytes(p) / 2);
-  k_cross_bwd_short<D><<<grid, shb::kThreads, shb::bytes<D>(P.lp), p.s>>>(mq, mg, mk, mv, mo, P);
+  k_cross_bwd_short<D><<<grid, shb::kThreads, shb::bytes<D>(P.lp, P.bufs), p.s>>>(mq, mg, mk, mv, mo, P);
   k_cross_sum_shares<<<dim3((unsigned)((p.l * D / 4 + 127) / 128), (unsigned)p.bh, 2), 128, 0, p.s>>>(
       P.part_k, P.part_v, P.l, P.lp, D, P.tiles, P.per, P.more, static_cast<__nv_bfloat16*>(dk),
       static_cast<__nv_bfloat16*>(dv));
