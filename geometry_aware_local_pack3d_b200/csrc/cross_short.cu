@@ -348,7 +348,7 @@ template <int D> constexpr int bytes(int lp, int bufs) {
          5 * Lay<D>::bytes(kTile) + 2 * kTile * 8 + 512;
 }
 // Buffers of P and dS: two where they fit, so that a tile's elementwise pass runs under the products
-// of the one before (65,536 rows x 8 heads to 77 states of 48: @@).
+// of the one before (65,536 rows x 8 heads to 77 states of 48: backward 88 -> 82 us).
 template <int D> constexpr int buffers(int lp) { return bytes<D>(lp, 2) <= sh::kSmem ? 2 : 1; }
 enum {
   B_Q = 0, B_KV = 2, B_KREADY, B_S, B_SFREE, B_ROWS, B_PD = B_ROWS + 2, B_MM = B_PD + 2,
@@ -437,6 +437,10 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
         tc::tmem_ld32(tl + 32 * h, s);
         tc::tmem_ld32(tl + cP + 32 * h, g);
         tc::tmem_wait_ld();
+        if (h + 1 == chunks) {  // S and dP have been read: the next tile's may be formed
+          tc::tc_fence_before();
+          arrive32(sb + 8 * B_SFREE);
+        }
         if (wh != 0xffffffffu) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
@@ -463,9 +467,7 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
           *reinterpret_cast<uint4*>(sd + at) = make_uint4(pd[0], pd[1], pd[2], pd[3]);
         }
       }
-      tc::tc_fence_before();
       tc::fence_proxy_async_smem();
-      arrive32(sb + 8 * B_SFREE);
       arrive32(sb + 8 * (B_PD + (n & 1)));
     }
   } else if (warp < 8) {
@@ -475,7 +477,8 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
     sh::Run ahead(P);
     bool ok = true;
     // the o row and lse of unit `ahead`: asked for a unit before they are used, since a trip to HBM
-    // per tile in this chain took as long as the tile (144 us of the training step below)
+    // per tile in this chain took as long as the tile (training step of 65,536 x 8 heads to 77 states of 48:
+    // 143 -> 126 us)
     uint4 orow[D / 8];
     float le = -INFINITY;
     auto fetch = [&]() {
