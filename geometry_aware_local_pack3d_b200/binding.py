@@ -658,7 +658,7 @@ _T = torch.Tensor
 
 def _tensor_list(ts, what, index):
     """Lengths, types and addresses of a list of tensors, each checked."""
-    if not all(map(_T.is_contiguous, ts)) or any([i != index for i in map(_T.get_device, ts)]):
+    if not all(map(_T.is_contiguous, ts)) or set(map(_T.get_device, ts)) - {index}:
         raise ValueError(f"{what} must be contiguous CUDA tensors on cuda:{index}")
     return list(map(_T.numel, ts)), [t.dtype for t in ts], array.array("Q", map(_T.data_ptr, ts))
 

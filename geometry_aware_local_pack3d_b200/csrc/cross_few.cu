@@ -8,7 +8,8 @@
 // time by asynchronous copies into its own two buffers (the next 12 KB in flight while it works, no
 // barrier with another warp), m16n8k16 products on registers, the softmax's maximum and sum in
 // registers (fp32). Masked states are not read at all: their copies fill zeros, chunks without a
-// state are left out, and the mask's bytes become words in the warp itself.
+// state are left out, and the mask's bytes become words in the warp itself: 25.5 us for the case above
+// with the join (75 MB in all, 2.9 TB/s).
 //
 // Chunks go to the warps of a problem in turn, so that a padded batch entry keeps all of them busy.
 // The block's warps join through shared memory, the blocks of a problem through k_cross_join.

@@ -14,6 +14,9 @@
 //   dk += dS^T q, which read the same tiles as MN-major operands (states along M). D = <dO, o> is
 //   taken from the rows as they pass. dk and dv stay in TMEM for the CTA's share of a problem's
 //   rows; the shares are added in order by k_cross_sum_shares (no atomics).
+// Measured: 2 x 8 heads of 32,768 rows to 77 padded states of 96, forward 48 us (4.2 TB/s of the 6.56
+// of a copy); 65,536 x 8 rows to 77 of 48, forward 38 us and backward 82 us (2.4 TB/s): there the chain
+// of a tile through its barriers is longer than its bytes take.
 // The mask is read as bytes by each CTA, once per problem: one bit per state in four words. Masked
 // logits become -inf, masked dS zero, and the masked rows of the tile that a product sums over (V
 // forward, K backward) are zeroed in shared memory, whatever they hold.
