@@ -286,3 +286,53 @@ def test_gradients_of_few_rows_over_a_long_context(d, B, H, HK, N, L, mask):
     f, g = run_and_check(q, k, v, m, dO)
     g2 = p3d().pack3d_cross_attn_bwd(q, k, v, f, dO, mask=m)
     assert all(torch.equal(g[n], g2[n]) for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("N,L", [(300, 77), (3000, 20), (20, 5000)])
+def test_wait_timeouts_of_short_contexts_and_split_states(N, L):
+    m3 = p3d()
+    q, k, v, m, dO = make(3, 4, 2, N, L, 96, torch.bfloat16, "random", seed=23)
+    f, g = run_and_check(q, k, v, m, dO)
+    torch.cuda.synchronize()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for call in ("fwd", "bwd"):
+        prev = m3.pack3d_testing_set_wait_budget(1)
+        try:
+            if call == "fwd":
+                m3.pack3d_cross_attn_fwd(q, k, v, mask=m, status=status)
+            else:
+                m3.pack3d_cross_attn_bwd(q, k, v, f, dO, mask=m, status=status)
+            torch.cuda.synchronize()
+        finally:
+            m3.pack3d_testing_set_wait_budget(prev)
+        assert m3.pack3d_read_status(status) == 6, call
+    f2, g2 = run_and_check(q, k, v, m, dO)
+    assert torch.equal(f["o"], f2["o"]) and all(torch.equal(g[n], g2[n]) for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("dtype,N,L", [(torch.float32, 2, 3000), (torch.bfloat16, 40, 5000),
+                                       (torch.bfloat16, 1, 1), (torch.float32, 300, 77)])
+def test_two_captured_graphs_replayed_in_turn(dtype, N, L):
+    # each graph has a workspace of its own, and replays see the inputs of the moment
+    m3 = p3d()
+    cases = [make(2, 4, 2, N, L, 64, dtype, "random", seed=s) for s in (31, 32)]
+    graphs, outs = [], []
+    for q, k, v, m, dO in cases:
+        run_and_check(q, k, v, m, dO)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            f = m3.pack3d_cross_attn_fwd(q, k, v, mask=m, save_for_backward=True)
+            g = m3.pack3d_cross_attn_bwd(q, k, v, f, dO, mask=m)
+        graphs.append(graph)
+        outs.append(dict(f, **g))
+    for i in (0, 1, 0):
+        graphs[i].replay()
+    for i in (0, 1):
+        q, k, v, m, dO = cases[i]
+        q.mul_(0.5)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        want = ob.cross(q, k, v, m, None, dO)
+        for n in ("o", "lse", "dq", "dk", "dv"):
+            ob.check(outs[i][n], want[n], n)
