@@ -7,8 +7,8 @@ raised.
 """
 from __future__ import annotations
 
-import array
 import ctypes
+import importlib.util
 import math
 import os
 
@@ -653,18 +653,27 @@ def pack3d_layer_norm_bwd(dy, x, weight, saved, *, weight_grad=True, bias_grad=T
     return dict(dx=dx, dweight=dw, dbias=db)
 
 
-_T = torch.Tensor
+_list_module = None
 
 
 def _tensor_list(ts, what, index):
-    """Lengths, types and addresses of a list of tensors, each checked."""
-    if not all(map(_T.is_contiguous, ts)) or set(map(_T.get_device, ts)) - {index}:
+    """Lengths, type codes and addresses of a list of tensors as bytes, each tensor checked."""
+    global _list_module
+    if _list_module is None:
+        path = os.path.join(os.path.dirname(_LIB_PATH), "_tensor_list.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} not found: run python -m geometry_aware_local_pack3d_b200.build")
+        spec = importlib.util.spec_from_file_location("_tensor_list", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _list_module = module
+    d = _list_module.describe(ts, index)
+    if d is None:
         raise ValueError(f"{what} must be contiguous CUDA tensors on cuda:{index}")
-    return list(map(_T.numel, ts)), [t.dtype for t in ts], array.array("Q", map(_T.data_ptr, ts))
-
-
-def _address(a):
-    return a.buffer_info()[0] if len(a) else None
+    if not d[3]:
+        other = next(t.dtype for t in ts if t.dtype not in _CODES)
+        raise TypeError(f"PACK3D supports float32 and bfloat16 tensors, got {other}")
+    return d[:3]
 
 
 def pack3d_grad_norm(grads, *, norm=None, workspace=None, stream=None, device=None):
@@ -694,18 +703,13 @@ def _grads(call, grads, clip, outs, max_norm, norm, workspace, stream, device):
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
             return _grads(call, grads, clip, outs, max_norm, norm, workspace, stream, like.device)
-    counts, dtypes, ptrs = _tensor_list(grads, "grads", index)
-    try:
-        codes = array.array("i", [_CODES[t] for t in dtypes])
-    except KeyError as e:
-        raise TypeError(f"PACK3D supports float32 and bfloat16 tensors, got {e.args[0]}") from None
+    counts, codes, ptrs = _tensor_list(grads, "grads", index)
     n = len(grads)
     to = ptrs
     if outs is not None:
-        to_counts, to_dtypes, to = _tensor_list(list(outs), "outs", index)
-        if to_counts != counts or to_dtypes != dtypes:
+        to_counts, to_codes, to = _tensor_list(list(outs), "outs", index)
+        if to_counts != counts or to_codes != codes:
             raise ValueError("outs must match grads in number, lengths and types")
-    counts = array.array("q", counts)
     if norm is None:
         norm = _new(stream, like, (1,), torch.float32)
     else:
@@ -714,12 +718,11 @@ def _grads(call, grads, clip, outs, max_norm, norm, workspace, stream, device):
     ws = _workspace(workspace, L_.pack3d_grad_norm_workspace_bytes(n), stream, like)
     s = _stream_of(index, stream)
     if clip:
-        st = L_.pack3d_clip_grad_norm(_address(ptrs), _address(to), _address(counts),
-                                      _address(codes), n, float(max_norm), norm.data_ptr(),
-                                      ws.data_ptr(), ws.numel(), s)
+        st = L_.pack3d_clip_grad_norm(ptrs, to, counts, codes, n, float(max_norm),
+                                      norm.data_ptr(), ws.data_ptr(), ws.numel(), s)
     else:
-        st = L_.pack3d_grad_norm(_address(ptrs), _address(counts), _address(codes), n,
-                                 norm.data_ptr(), ws.data_ptr(), ws.numel(), s)
+        st = L_.pack3d_grad_norm(ptrs, counts, codes, n, norm.data_ptr(), ws.data_ptr(),
+                                 ws.numel(), s)
     if st != PACK3D_OK:
         raise Pack3DError(st, call)
     return norm

@@ -1,4 +1,5 @@
-"""Build step: compile the CUDA sources of the package into lib/libpack3d.so for sm_100a.
+"""Build step: compile the CUDA sources of the package into lib/libpack3d.so for sm_100a, and the
+binding's helper for lists of tensors into lib/_tensor_list.so.
 
 Usage: python -m geometry_aware_local_pack3d_b200.build [--force] [--verbose]
 Objects go to _build/ (git-ignored); the shared library is written in-tree so it travels
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "lib", "libpack3d.so")
+LIST_SRC = os.path.join(CSRC, "tensor_list.cpp")
+LIST_LIB = os.path.join(PKG, "lib", "_tensor_list.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3",
@@ -53,9 +57,31 @@ def _compile(src, verbose, extra):
     return obj, r.stderr
 
 
+def build_tensor_list(force=False):
+    """The host helper that reads a list of tensors (a CPython module over torch's headers)."""
+    newest = max(os.path.getmtime(LIST_SRC), os.path.getmtime(__file__))
+    if not force and os.path.exists(LIST_LIB) and os.path.getmtime(LIST_LIB) >= newest:
+        return LIST_LIB
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = LIST_LIB + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], LIST_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {LIST_SRC}:\n{r.stderr}")
+    os.replace(tmp, LIST_LIB)
+    return LIST_LIB
+
+
 def build(force=False, verbose=False, extra=()):
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
+    build_tensor_list(force)
     srcs = sources()
     newest = max(os.path.getmtime(p) for p in srcs + headers() + [__file__])
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:

@@ -188,3 +188,13 @@ def test_binding_refuses_a_stream_of_another_device():
     assert b._stream_of(1, Stream) == 7
     with pytest.raises(ValueError):
         b._stream_of(0, Stream)
+
+
+def test_list_helper_refuses_what_is_no_dense_tensor_of_the_device():
+    t = torch.zeros(4)
+    for bad in ([t], [t.to_sparse()], [torch.zeros(4, device="meta")], [torch.zeros(4, 4).t()]):
+        with pytest.raises(ValueError):
+            b._tensor_list(bad, "grads", 0)
+    with pytest.raises(TypeError):
+        b._tensor_list([t, None][1:], "grads", 0)
+    assert b._tensor_list([], "grads", 0) == (b"", b"", b"")
