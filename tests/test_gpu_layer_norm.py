@@ -121,3 +121,9 @@ def test_gradient_against_differences():
             vals.append(float((y.double() * dy.double()).sum()))
         got, want = (vals[0] - vals[1]) / (2 * h), float((g[name].double() * t.double()).sum())
         assert abs(got - want) <= 5e-3 * (1 + abs(want)), name
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(30001, 3), (20001, 9), (9001, 31), (5001, 333), (3001, 511), (1, 257)])
+def test_ragged_widths_over_many_rows(dtype, rows, cols):
+    run_and_check(*make(rows, cols, dtype, torch.float32))
