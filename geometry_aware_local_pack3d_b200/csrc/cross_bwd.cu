@@ -24,6 +24,7 @@
 // the masked rows' sums are simply not written and zeros are.
 #include <math.h>
 
+#include "cross_phases.h"
 #include "cross_tc.cuh"
 #include "launch.h"
 
@@ -484,7 +485,8 @@ template <int D> struct Smem {
   static constexpr int TB = Lay<D>::bytes(kTile), HB = Lay<D>::bytes(xb::kHalf);
   static constexpr int kK = 0, kV = TB, kRing = 2 * TB;
   static constexpr int kRowB = xb::kHalf * 8;               // (-lse log2(e), D tau) of a step's rows
-  static constexpr int kStages = D <= 96 ? 6 : 4;  // even: a group of warps sees the same slots
+  static constexpr int kStages = dkv_stages(D);
+  static_assert(kStages % 2 == 0, "a group of warps sees the same slots");
   static constexpr int kRows = kRing + kStages * 2 * HB;    // [stages]
   static constexpr int kBar = kRows + kStages * kRowB;
   static constexpr int kBytes = kBar + 512;
@@ -492,7 +494,8 @@ template <int D> struct Smem {
 constexpr int kMaxStages = 6;
 enum {
   B_AFULL = 0, B_QFULL = 1, B_QEMPTY = B_QFULL + kMaxStages, B_SFULL = B_QEMPTY + kMaxStages,
-  B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_DONE = B_PFULL + 2, B_ALL = B_DONE + 2, B_DRAIN, B_COUNT
+  B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_DONE = B_PFULL + kDkvTurns,
+  B_ALL = B_DONE + kDkvTurns, B_DRAIN, B_COUNT
 };
 static_assert(8 * B_COUNT + 16 <= 512, "barrier area");
 // TMEM columns: dk, dv and slots of 64. Step i has S^T in slot s(i), over which its P and dS (bf16)
@@ -501,7 +504,7 @@ static_assert(8 * B_COUNT + 16 <= 512, "barrier area");
 // that the products of steps i and i + 2 need not wait for one another. At d = 128 there are four:
 // steps i and i + 2 share theirs.
 template <int D> struct Cols {
-  static constexpr bool kFive = D <= 96;
+  static constexpr bool kFive = dkv_five(D);
   static constexpr uint32_t kK = 0, kV = D, kS = 2 * D;
   static_assert(kS + 64 * (kFive ? 5 : 4) <= 512, "tensor memory");
   __device__ __forceinline__ static uint32_t s(int i) {
@@ -551,6 +554,8 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars[B_SFULL + i], 1);
       tc::mbar_init(&bars[B_SFREE + i], 128);
+    }
+    for (int i = 0; i < kDkvTurns; ++i) {
       tc::mbar_init(&bars[B_PFULL + i], 128);
       tc::mbar_init(&bars[B_DONE + i], 1);
     }
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
       seen = C::kFive ? ab.probe(sb + 8 * (B_SFULL + b), (i >> 1) + 1) : 0u;
       tc::tmem_wait_st();
       tc::tc_fence_before();
-      arrive32(sb + 8 * (B_PFULL + b));
+      arrive32(sb + 8 * (B_PFULL + i % kDkvTurns));
     }
     // warps 0-3 write dk, warps 4-7 dv, once every step's products have completed (a barrier of
     // its own: a group has not followed the other group's phases of B_DONE)
@@ -698,7 +703,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
       // four slots, the products of step i - 2
       const int done = i - (C::kFive ? 3 : 2);
       if (C::kFive && i >= 2) ok = ok && ab.all(sb + 8 * (B_SFREE + b), (i - 2) >> 1);
-      if (done >= 0) ok = ok && ab.all(sb + 8 * (B_DONE + (done & 1)), done >> 1);
+      if (done >= 0) ok = ok && ab.all(sb + 8 * (B_DONE + done % kDkvTurns), done / kDkvTurns);
       if (!ok) break;
       tc::tc_fence_after();
       if (tc::elect_one()) {
@@ -725,8 +730,8 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
     constexpr uint64_t HO = (uint64_t)(S::HB >> 4);
 #pragma unroll 1
     for (int i = 0; i < NT; ++i) {
-      const int st = i % kStages, b = i & 1;
-      if (!ab.all(sb + 8 * (B_PFULL + b), i >> 1)) break;
+      const int st = i % kStages, turn = i % kDkvTurns;
+      if (!ab.all(sb + 8 * (B_PFULL + turn), i / kDkvTurns)) break;
       tc::tc_fence_after();
       if (tc::elect_one()) {
         const uint64_t qm = r0 + 2 * st * HO, gm = qm + HO;
@@ -738,7 +743,7 @@ __global__ void __launch_bounds__(xk::kThreads, 1)
                      (i > 0 || ks > 0) ? 1u : 0u);
         }
         commit32(sb + 8 * (B_QEMPTY + st));
-        commit32(sb + 8 * (B_DONE + b));
+        commit32(sb + 8 * (B_DONE + turn));
         if (i == NT - 1) commit32(sb + 8 * (B_ALL));
       }
       __syncwarp();
