@@ -5,11 +5,10 @@
 #pragma once
 
 #include "common.cuh"
+#include "cross_phases.h"
 
 namespace p3d {
 namespace xa {
-
-constexpr int kTile = 128;  // rows or states of a tile
 
 struct Problem {
   const void *q, *k, *v;
@@ -52,12 +51,9 @@ inline size_t mask_bytes(const Problem& p, int tw) {
          align256(sizeof(uint32_t) * p.batch * m.words);
 }
 
-// States per tile of the forward on tensor cores: two buffers of S (one at d = 128), P (bf16, half
-// as many columns) and O of a row tile take half of the 512 columns of TMEM.
-constexpr int fwd_tile(int) { return 64; }
 // Words per tile of the mask's list, forward and backward.
 inline int mask_tile_words(const Problem& p, bool backward) {
-  return !backward && p.dtype == PACK3D_BF16 ? fwd_tile(p.d) / 32 : kTile / 32;
+  return !backward && p.dtype == PACK3D_BF16 ? kFwdTile / 32 : kTile / 32;
 }
 
 cudaError_t build_mask(const Problem& p, const MaskTables& m);

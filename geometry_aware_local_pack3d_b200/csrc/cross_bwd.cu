@@ -24,7 +24,6 @@
 // the masked rows' sums are simply not written and zeros are.
 #include <math.h>
 
-#include "cross_phases.h"
 #include "cross_tc.cuh"
 #include "launch.h"
 
@@ -75,14 +74,13 @@ static_assert(128 * (kMore + kLess) <= kThreads * kRegs, "registers of the launc
 template <int D> struct Smem {
   static constexpr int TB = Lay<D>::bytes(kTile), HB = Lay<D>::bytes(xb::kHalf);
   static constexpr int kQ = 0, kG = TB, kRing = 2 * TB;
-  // two CTAs per SM: 2 (bytes + 1 KB) within 228 KB
-  static constexpr int kFit = (116736 - 1024 - 512 - kRing) / HB;
   // V and K take turns (V first: its slot is free before K's, which the step's last product reads)
-  static constexpr int kSlots = kFit < 6 ? kFit : 6;
+  static constexpr int kSlots = dq_slots(D);
+  static_assert(kRing == dq_ring_at(D), "shared memory");
   static constexpr int kBar = kRing + kSlots * HB;
   static constexpr int kBytes = kBar + 512;
 };
-constexpr int kMaxSlots = 6, kReady = 8;
+constexpr int kMaxSlots = 6, kReady = kDqReady;
 enum {
   B_QFULL = 0, B_QEMPTY = 1, B_FULL = 2, B_EMPTY = B_FULL + kMaxSlots,
   B_READY = B_EMPTY + kMaxSlots, B_SFULL = B_READY + kReady, B_SFREE, B_PFULL, B_DONE, B_STAGED,
@@ -93,7 +91,7 @@ static_assert(8 * B_COUNT + 16 <= 512, "barrier area");
 // step's S and dP are formed as soon as this step's have been read; at d = 128 dS lies over S and
 // they wait for this step's last product.
 template <int D> struct Cols {
-  static constexpr bool kOwn = D <= 96;
+  static constexpr bool kOwn = dq_own(D);
   static constexpr uint32_t kS = 0, kP = 64, kD = kOwn ? 128 : 0, kO = kOwn ? 160 : 128;
   static_assert(kO + D <= 256, "tensor memory");
 };

@@ -4,7 +4,7 @@
 //   lse_i = log sum_j exp s_ij;   a row with no unmasked state has o = 0, lse = -inf.
 //
 // Work unit: 256 rows of one problem = two 128-row tiles that share every K and V tile of KT = 64
-// states (see fwd_tile). Persistent CTAs of 18 warps:
+// states. Persistent CTAs of 18 warps:
 //   0-3, 4-7  softmax of tile 0 and 1 (thread = row = TMEM lane)
 //   8-11      epilogue of both tiles: O / sum in bf16, through the tile's consumed q rows, by TMA
 //   12        TMA loads;  13, 14  S products of tile 0 and 1;  15, 16  O products of them
@@ -43,27 +43,26 @@ constexpr int kThreads = 640;  // whole groups of four warps (two warps idle): t
 // block's.
 constexpr int kRegs = 96, kMore = 144, kLess = 64;
 static_assert(256 * kMore + (kThreads - 256) * kLess <= kThreads * kRegs, "registers of the block");
-constexpr int kSmemLimit = 232448;
 template <int D> struct Smem {
-  static constexpr int KT = fwd_tile(D);               // states per tile
+  static constexpr int KT = kFwdTile;                  // states per tile
   static constexpr int QB = Lay<D>::bytes(kTile), KB = Lay<D>::bytes(KT);
   static constexpr int kSum = 0;                       // [2 turns][2 tiles][128] row sums
   static constexpr int kRef = kSum + 2048;             // the same of the references
   static constexpr int kQ = kRef + 2048;               // [2 buffers][2 tiles]
   static constexpr int kRing = kQ + 4 * QB;
-  static constexpr int kFit = (kSmemLimit - 1024 - 512 - kRing) / KB;
-  static constexpr int kSlots = kFit < 8 ? kFit : 8;   // K and V tiles take turns
+  static constexpr int kSlots = fwd_slots(D);          // K and V tiles take turns
   static constexpr int kBar = kRing + kSlots * KB;
   static constexpr int kBytes = kBar + 512 + 1024;     // + room to align the base to 1,024
   // TMEM columns of tile t: S, P, O at t * 256 + ...
-  static constexpr int kBufs = D <= 96 ? 2 : 1;        // of S
+  static constexpr int kBufs = fwd_bufs(D);            // of S
   static constexpr uint32_t kS = 0, kP = kBufs * KT, kO = kP + KT / 2;
   static_assert(kO + D <= 256, "tensor memory of a tile");
-  static_assert(kSlots >= 4, "two K and two V tiles");
+  static_assert(kRing == fwd_ring_at(D) && kBytes <= kSmemLimit, "shared memory");
+  static_assert(kSlots >= 4 && kSlots % 2 == 0, "two K and two V tiles, each in slots of their own");
 };
 constexpr int kMaxSlots = 8;
 // V tiles the row-clearing warp may be ahead of the MMA warps: fewer than the ring holds
-constexpr int kReady = 8;
+constexpr int kReady = kFwdReady;
 enum {
   B_QFULL = 0, B_QEMPTY = 4, B_FULL = 8, B_EMPTY = B_FULL + kMaxSlots,
   B_READY = B_EMPTY + kMaxSlots, B_SFULL = B_READY + kReady, B_SFREE = B_SFULL + 4,
@@ -775,7 +774,7 @@ cudaError_t build_mask(const Problem& p, const MaskTables& m) {
 // State ranges per unit: only when the units leave SMs idle, at least two tiles each.
 static int fwd_splits(const Problem& p) {
   const int64_t units = p.bh * ((p.np + 2 * kTile - 1) / (2 * kTile));
-  const int64_t tiles = (p.l + fwd_tile(p.d) - 1) / fwd_tile(p.d);
+  const int64_t tiles = (p.l + kFwdTile - 1) / kFwdTile;
   const int64_t room = sm_count() / (units > 0 ? units : 1);
   int64_t n = tiles / 2 < room ? tiles / 2 : room;
   if (n > kMaxSplits) n = kMaxSplits;
