@@ -54,5 +54,11 @@ constexpr bool dkv_five(int d) { return d <= 96; }
 // scores wait for the products of step i + 1.
 constexpr int kDkvTurns = 4;
 
+// ---- k_cross_fwd_short (o, lse of at most 128 states)
+// Barriers of staged output rows, in turn as the two buffers of rows are. With one, the rows of tile
+// n + 1, which wait for the store of tile n - 1 alone, could complete the next phase while the
+// storing warp still waits for those of tile n.
+constexpr int kShortTurns = 2;
+
 }  // namespace xa
 }  // namespace p3d

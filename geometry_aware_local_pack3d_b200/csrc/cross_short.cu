@@ -106,7 +106,8 @@ template <int D> constexpr int bytes(int lp) {
   return 2 * Lay<D>::bytes(kTile) + 2 * Lay<D>::bytes(lp) + 256 + 1024;
 }
 enum {
-  B_Q = 0, B_QFREE = 2, B_KV = 4, B_VREADY, B_S, B_P, B_O, B_STAGED, B_DRAIN, B_COUNT
+  B_Q = 0, B_QFREE = 2, B_KV = 4, B_VREADY, B_S, B_P, B_O, B_STAGED, B_DRAIN = B_STAGED + kShortTurns,
+  B_COUNT
 };
 constexpr uint32_t kS = 0, kO = 128;  // TMEM columns (of 256): S, then P over it; O
 }  // namespace shf
@@ -133,7 +134,8 @@ __global__ void __launch_bounds__(shf::kThreads, 2)
   const uint32_t sb = tc::smem_u32(bars);  // barrier i at sb + 8 i
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i)
-      tc::mbar_init(&bars[i], i == B_P || i == B_VREADY || i == B_STAGED ? 128 : 1);
+      tc::mbar_init(&bars[i],
+                    i == B_P || i == B_VREADY || (i >= B_STAGED && i < B_DRAIN) ? 128 : 1);
     abort_flag[0] = 0;
     tc::fence_mbar_init();
   }
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(shf::kThreads, 2)
       }
       tc::tc_fence_before();
       tc::fence_proxy_async_smem();
-      arrive32(sb + 8 * B_STAGED);
+      arrive32(sb + 8 * (B_STAGED + n % kShortTurns));
     }
   } else if (warp == 4) {
     // ------------------------------------------------------------ loads and products
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(shf::kThreads, 2)
       uint32_t n = 0;
 #pragma unroll 1
       for (sh::Run R(P); R.left > 0; R.next(P), ++n) {
-        if (!ab.wait(sb + 8 * B_STAGED, n)) break;
+        if (!ab.wait(sb + 8 * (B_STAGED + n % kShortTurns), n / kShortTurns)) break;
 #pragma unroll 1
         for (int c = 0; c < Ly::NB; ++c)
           tma_store_3d(&mo, smem + (n & 1) * QB + c * kTile * Ly::RB, c * Ly::CW, R.tile * kTile,

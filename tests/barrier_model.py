@@ -569,6 +569,81 @@ def dkv(c, steps):
     return m
 
 
+# ------------------------------------------------------------------ k_cross_fwd_short
+def forward_short(c, run):
+    """run: row tiles of each problem that the CTA walks. c: staged (barriers of staged rows)."""
+    m = Machine()
+    NG = c["staged"]
+    units = [(p, i) for p, n in enumerate(run) for i in range(n)]
+    for n, k in (("KV", 1), ("VREADY", 4), ("S", 1), ("P", 4), ("O", 1)):
+        m.bar(n, k)
+    for i in range(2):
+        m.bar(("Q", i))
+        m.bar(("QFREE", i))
+    for i in range(NG):
+        m.bar(("STAGED", i), 4)
+
+    def softmax(w):
+        for n, (p, i) in enumerate(units):
+            if i == 0:
+                yield "wait", "KV", p
+                yield "read", ("KV", w), p
+                yield "write", ("KV", w), ("cleared", p)
+                yield "arrive", "VREADY"
+            yield "wait", "S", n
+            yield "read", ("S", w), ("S", n)
+            yield "write", ("S", w), ("P", n)
+            yield "arrive", "P"
+            yield "wait", "O", n
+            yield "read", ("O",), n
+            yield "write", ("Q", n & 1, w), ("out", n)
+            yield "arrive", ("STAGED", n % NG)
+
+    def products():
+        gen = 0
+
+        def load(i):
+            for x in range(3):
+                yield "write", ("Q", i & 1, x), i
+            yield "copy", "Q", ("Q", i & 1, 3), i, ("Q", i & 1)
+
+        yield from load(0)
+        for n, (p, i) in enumerate(units):
+            if n:
+                yield "wait", "O", n - 1
+            if i == 0:
+                for x in range(3):
+                    yield "write", ("KV", x), p
+                yield "copy", "KV", ("KV", 3), p, "KV"
+                yield "wait", "KV", gen
+                gen += 1
+            yield "wait", ("Q", n & 1), n >> 1
+            yield "products", [(("Q", n & 1, x), n) for x in range(4)], [(("S", w), ("S", n), 0) for w in range(4)], \
+                ["S"]
+            if n + 1 < len(units):
+                if n >= 1:
+                    yield "wait", ("QFREE", (n + 1) & 1), ((n + 1) >> 1) - 1
+                yield from load(n + 1)
+            if i == 0:
+                yield "wait", "VREADY", gen - 1
+            yield "wait", "P", n
+            yield "products", [(("S", w), ("P", n)) for w in range(4)] + \
+                [(("KV", w), ("cleared", p)) for w in range(4)], [(("O",), n, 0)], ["O"]
+
+    def stores():
+        for n in range(len(units)):
+            yield "wait", ("STAGED", n % NG), n // NG
+            for x in range(4):
+                yield "store", ("Q", n & 1, x), ("out", n)
+            yield "arrive", ("QFREE", n & 1)
+
+    for w in range(4):
+        m.agent(f"softmax {w}", softmax(w))
+    m.agent("products", products())
+    m.agent("stores", stores())
+    return m
+
+
 # ------------------------------------------------------------------ k_cross_bwd_short
 def backward_short(c, run):
     """run: row tiles of each problem that the CTA walks. c: bufs (buffers of P and dS)."""

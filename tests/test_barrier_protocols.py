@@ -26,6 +26,7 @@ int dq_ready() { return kDqReady; }
 int dkv_stages_of(int d) { return dkv_stages(d); }
 int dkv_five_of(int d) { return dkv_five(d); }
 int dkv_turns() { return kDkvTurns; }
+int short_turns() { return kShortTurns; }
 }
 """
 
@@ -112,6 +113,13 @@ def test_an_odd_ring_is_noticed(units, masked):
 def test_dq_kernel(numbers, d, masked, units):
     holds(bm.dq, (("slots", numbers.dq_slots_of(d)), ("ready", numbers.dq_ready()),
                   ("own", bool(numbers.dq_own_of(d)))), units, masked)
+
+
+@pytest.mark.parametrize("run", [(5,), (1, 1, 1, 1), (3, 2, 4)])
+def test_short_forward_kernel(numbers, run):
+    holds(bm.forward_short, (("staged", numbers.short_turns()),), run)
+    with pytest.raises(bm.Violation):  # one barrier for both buffers of rows is too few
+        bm.check(lambda: bm.forward_short(dict(staged=1), run))
 
 
 @pytest.mark.parametrize("bufs", [1, 2])
