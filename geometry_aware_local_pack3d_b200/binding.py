@@ -130,6 +130,8 @@ def lib():
         L.pack3d_last_launch_count.argtypes = []
         L.pack3d_testing_set_wait_budget.restype = ctypes.c_longlong
         L.pack3d_testing_set_wait_budget.argtypes = [ctypes.c_longlong]
+        L.pack3d_testing_wait.restype = st
+        L.pack3d_testing_wait.argtypes = [_P, _P]
         _lib = L
     return _lib
 
@@ -739,6 +741,14 @@ def pack3d_last_launch_count():
 def pack3d_testing_set_wait_budget(cycles):
     """Testing hook: SM-cycle budget of the kernels' device-side waits (<= 0: default)."""
     return int(lib().pack3d_testing_set_wait_budget(int(cycles)))
+
+
+def pack3d_testing_wait():
+    """Runs a wait that nothing ends with the budget of the moment: (gave up, cycles it took)."""
+    out = torch.zeros(2, dtype=torch.int64, device="cuda")
+    _check(lib().pack3d_testing_wait(out.data_ptr(), _stream()), "pack3d_testing_wait")
+    gave_up, cycles = out.tolist()
+    return bool(gave_up), cycles
 
 
 def pack3d_strerror(status):

@@ -57,6 +57,7 @@ inline int mask_tile_words(const Problem& p, bool backward) {
 }
 
 cudaError_t build_mask(const Problem& p, const MaskTables& m);
+cudaError_t wait_in_vain(long long* out, cudaStream_t s);  // testing
 
 // forward (o, lse), bf16 and fp32; `ws` follows the mask's tables
 size_t fwd_tc_bytes(const Problem& p);

@@ -179,3 +179,10 @@ extern "C" pack3d_status pack3d_read_status(int32_t* status, void* stream) {
   if (h != 0 && cudaMemsetAsync(status, 0, sizeof(h), s) != cudaSuccess) return PACK3D_ERR_CUDA;
   return static_cast<pack3d_status>(h);
 }
+
+extern "C" pack3d_status pack3d_testing_wait(int64_t* out, void* stream) {
+  reset_launches();
+  if (!out) return PACK3D_ERR_INVALID_ARG;
+  return cuda_status(xa::wait_in_vain(reinterpret_cast<long long*>(out),
+                                      static_cast<cudaStream_t>(stream)));
+}

@@ -764,6 +764,32 @@ __global__ void __launch_bounds__(512)
   if (threadIdx.x == 0) list[0] = total;
 }
 
+// A wait for a barrier on which nothing arrives (pack3d_testing_wait): out = gave up, cycles.
+__global__ void __launch_bounds__(32) k_cross_wait(long long budget, long long* __restrict__ out) {
+  __shared__ uint64_t bar;
+  __shared__ int flag;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bar, 1);
+    flag = 0;
+    tc::fence_mbar_init();
+  }
+  __syncwarp();
+  const Waiter ab(&flag, budget);
+  const long long t0 = clock64();
+  const bool ok = ab.all(tc::smem_u32(&bar), 0);
+  const long long t = clock64() - t0;
+  if (threadIdx.x == 0) {
+    out[0] = !ok && *const_cast<volatile int*>(&flag) == 1;
+    out[1] = t;
+  }
+}
+
+cudaError_t wait_in_vain(long long* out, cudaStream_t s) {
+  k_cross_wait<<<1, 32, 0, s>>>(wait_budget_cycles(), out);
+  count_launch();
+  return cudaGetLastError();
+}
+
 cudaError_t build_mask(const Problem& p, const MaskTables& m) {
   if (!m.act) return cudaSuccess;
   k_cross_mask<<<p.batch, 512, 0, p.s>>>(p.mask, p.l, m.tiles, m.tw, m.words, m.act, m.bits);

@@ -104,34 +104,36 @@ __device__ __forceinline__ void commit32(uint32_t bar) {
                : "memory");
 }
 
-// Bounded, abortable wait (as tc::Abort) that suspends on the barrier instead of polling it: a
-// polling warp takes issue slots from the warps of its sub-partition that compute. A wait that runs
-// out raises the CTA's abort word, every other wait then gives up, and the kernel records
-// PACK3D_ERR_TIMEOUT once at its end. The wait is inlined at many places and stays short: these
-// kernels have many roles, and code beyond the instruction cache costs them more than waiting.
+// Bounded, abortable wait (as tc::Abort: `budget` SM clock cycles from the first look that fails)
+// that suspends on the barrier instead of polling it: a polling warp takes issue slots from the warps
+// of its sub-partition that compute. A suspension lasts kNap ns at most, so a wait outlasts its budget
+// by about that. A wait that runs out raises the CTA's abort word, every other wait then gives up, and
+// the kernel records PACK3D_ERR_TIMEOUT once at its end. The wait is inlined at many places and stays
+// short: these kernels have many roles, and code beyond the instruction cache costs them more than
+// waiting.
 struct Waiter {
-  uint32_t flag;   // shared address of the abort word
-  uint32_t hint;   // nanoseconds of one suspension: a millisecond, or less for a small budget
-  uint32_t tries;  // suspensions that use up the budget, of 2,000 cycles or more each
-  __device__ __forceinline__ Waiter(volatile int* f, long long budget)
-      : flag(tc::smem_u32(const_cast<int*>(f))),
-        hint(budget < 1000000 ? (uint32_t)budget : 1000000u),
-        tries((uint32_t)(budget / 2000 < 100000000 ? budget / 2000 : 100000000)) {}
+  static constexpr uint32_t kNap = 20000;
+  uint32_t flag;     // shared address of the abort word
+  long long budget;  // cycles
+  __device__ __forceinline__ Waiter(volatile int* f, long long b)
+      : flag(tc::smem_u32(const_cast<int*>(f))), budget(b) {}
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase) const {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
-        "mov.u32 n, %4;\n\tmov.u32 %0, 1;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 f;\n\t.reg .u64 t0, t;\n\t"
+        "mov.u32 %0, 1;\n\t"
         "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra DONE;\n"
+        "@p bra DONE;\n\t"
+        "mov.u64 t0, %%clock64;\n"
         "WAIT:\n\t"
-        "ld.volatile.shared.u32 f, [%5];\n\t"
+        "ld.volatile.shared.u32 f, [%4];\n\t"
         "setp.ne.u32 q, f, 0;\n\t"
         "@q bra FAIL;\n\t"
-        "setp.eq.u32 q, n, 0;\n\t"
-        "@q st.volatile.shared.u32 [%5], 1;\n\t"
+        "mov.u64 t, %%clock64;\n\t"
+        "sub.u64 t, t, t0;\n\t"
+        "setp.gt.s64 q, t, %5;\n\t"
+        "@q st.volatile.shared.u32 [%4], 1;\n\t"
         "@q bra FAIL;\n\t"
-        "sub.u32 n, n, 1;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "@!p bra WAIT;\n\t"
         "bra DONE;\n"
@@ -139,7 +141,7 @@ struct Waiter {
         "mov.u32 %0, 0;\n"
         "DONE:\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(phase & 1), "r"(hint), "r"(tries), "r"(flag)
+        : "r"(bar), "r"(phase & 1), "r"(kNap), "r"(flag), "l"(budget)
         : "memory");
     return ok != 0;
   }

@@ -388,6 +388,11 @@ int pack3d_last_launch_count(void);
  * it exists so that tests can exercise that path without faulting or hanging a GPU. */
 long long pack3d_testing_set_wait_budget(long long cycles);
 
+/* TESTING HOOK. One warp waits, as the warps of the cross-attention kernels do and with the budget
+ * of the moment, for a barrier on which nothing ever arrives. out: device int64 [2]: 1 if the wait
+ * gave up, and the SM clock cycles that it took (more than the budget by well below a millisecond). */
+pack3d_status pack3d_testing_wait(int64_t* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -336,3 +336,16 @@ def test_two_captured_graphs_replayed_in_turn(dtype, N, L):
         want = ob.cross(q, k, v, m, None, dO)
         for n in ("o", "lse", "dq", "dk", "dv"):
             ob.check(outs[i][n], want[n], n)
+
+
+@pytest.mark.parametrize("budget", [10_000, 2_000_000, 200_000_000])
+def test_a_wait_gives_up_after_its_budget(budget):
+    # a barrier on which nothing arrives: the wait ends after the budget (0.1 s at most here) and at most
+    # 0.2 ms later, ten times its longest nap of 20 us, at 2 GHz
+    m3 = p3d()
+    prev = m3.pack3d_testing_set_wait_budget(budget)
+    try:
+        gave_up, cycles = m3.pack3d_testing_wait()
+    finally:
+        m3.pack3d_testing_set_wait_budget(prev)
+    assert gave_up and budget < cycles <= budget + 400_000

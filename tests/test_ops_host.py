@@ -54,6 +54,11 @@ def test_cross_backward_refusals(kw, status):
     assert b.lib().pack3d_last_launch_count() == 0
 
 
+def test_the_wait_hook_refuses_a_null_pointer():
+    assert b.lib().pack3d_testing_wait(None, None) == 1
+    assert b.lib().pack3d_last_launch_count() == 0
+
+
 def test_cross_workspace_sizes():
     f = b.pack3d_cross_attn_workspace_bytes
     assert f(1, 1, 2, 2, 10, 10, 50) == 0 and f(1, 1, 3, 2, 10, 10, 96) == 0
