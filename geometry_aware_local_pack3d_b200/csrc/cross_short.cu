@@ -513,9 +513,9 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
           for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
         }
       }
-      // a row without any state, and the rows past the last: P = 0
-      srow[(i & 1) * kTile + rin] =
-          make_float2(le == -INFINITY ? -INFINITY : -le * kLog2e, s * P.scale);
+      // a row without any state, and the rows past the last: P = 0, and no D of whatever dO holds
+      srow[(i & 1) * kTile + rin] = le == -INFINITY ? make_float2(-INFINITY, 0.f)
+                                                    : make_float2(-le * kLog2e, s * P.scale);
       arrive32(sb + 8 * (B_ROWS + (i & 1)));
       ahead.next(P);
       fetch();
@@ -715,10 +715,12 @@ __global__ void __launch_bounds__(shb::kThreads, 1)
 }
 
 // dk, dv of problem blockIdx.y: the shares of the CTAs c0 .. c1 that walked its rows, in order. Four
-// elements per thread.
+// elements per thread. A masked state's are zero by selection: its shares hold 0 x dO and 0 x q, which
+// are no zeros where a row is not finite.
 __global__ void __launch_bounds__(128)
-    k_cross_sum_shares(const float* __restrict__ pk, const float* __restrict__ pv, int l, int lp,
-                       int d, int tiles, int per, int more, __nv_bfloat16* __restrict__ dk,
+    k_cross_sum_shares(const float* __restrict__ pk, const float* __restrict__ pv,
+                       const uint8_t* __restrict__ mask, int kv_heads, int l, int lp, int d,
+                       int tiles, int per, int more, __nv_bfloat16* __restrict__ dk,
                        __nv_bfloat16* __restrict__ dv) {
   const int e = (blockIdx.x * 128 + threadIdx.x) * 4, bh = blockIdx.y;
   if (e >= l * d) return;
@@ -729,12 +731,14 @@ __global__ void __launch_bounds__(128)
   };
   const int c0 = cta(bh * tiles), c1 = cta(bh * tiles + tiles - 1);
   const float* p = (blockIdx.z ? pv : pk) + (int64_t)bh * lp * d + e;
+  const bool in = !mask || mask[(int64_t)(bh / kv_heads) * l + e / d] != 0;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int c = c0; c <= c1; ++c) {
     const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)c * lp * d);
     s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
   }
+  if (!in) s = make_float4(0.f, 0.f, 0.f, 0.f);
   *reinterpret_cast<uint2*>((blockIdx.z ? dv : dk) + (int64_t)bh * l * d + e) =
       make_uint2(tc::pack_bf16(s.x, s.y), tc::pack_bf16(s.z, s.w));
 }
@@ -830,7 +834,7 @@ static cudaError_t launch_bwd_short(const Problem& p, const void* o, const float
   P.part_v = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + bwd_short_bytes(p) / 2);
   k_cross_bwd_short<D><<<grid, shb::kThreads, shb::bytes<D>(P.lp, P.bufs), p.s>>>(mq, mg, mk, mv, mo, P);
   k_cross_sum_shares<<<dim3((unsigned)((p.l * D / 4 + 127) / 128), (unsigned)p.bh, 2), 128, 0, p.s>>>(
-      P.part_k, P.part_v, P.l, P.lp, D, P.tiles, P.per, P.more, static_cast<__nv_bfloat16*>(dk),
+      P.part_k, P.part_v, P.mask, P.kv_heads, P.l, P.lp, D, P.tiles, P.per, P.more, static_cast<__nv_bfloat16*>(dk),
       static_cast<__nv_bfloat16*>(dv));
   count_launch(2);
   return cudaGetLastError();

@@ -433,6 +433,11 @@ __global__ void __launch_bounds__(xs::kThreads, D <= 64 ? 2 : 1) k_cross_dkv32(c
     const int64_t row = at + 4 * ty + i;
     if (row >= P.l) continue;
     const int64_t dst = ((split * P.bh + bh) * P.l + row) * D;
+    if (!on(w0, w1, 4 * ty + i)) {
+      // a masked state: zeros, not 0 x dO and 0 x q of rows that may not be finite
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
+    }
     store_columns<D>(P.dk + dst, tx, ak[i], 1.f);
     store_columns<D>(P.dv + dst, tx, av[i], 1.f);
   }

@@ -349,3 +349,33 @@ def test_a_wait_gives_up_after_its_budget(budget):
     finally:
         m3.pack3d_testing_set_wait_budget(prev)
     assert gave_up and budget < cycles <= budget + 400_000
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("mask", ["random", "empty"])
+@pytest.mark.parametrize("N,L,d", [(300, 77, 96), (130, 20, 48), (200, 128, 64), (40, 100, 128), (150, 300, 96),
+                                   (2, 500, 48), (1000, 2000, 64)])
+def test_rows_that_are_not_finite_keep_to_their_own_gradients(dtype, mask, N, L, d):
+    # an infinity in dO and a NaN in q: gradients of states left out stay 0, as do those of rows
+    # without any state, and every row and batch entry without one is as it was
+    q, k, v, m, dO = make(3, 4, 2, N, L, d, dtype, mask, seed=41, garbage=True)
+    if mask == "random":
+        m[1] = False  # the entry in the middle has no state
+    f = p3d().pack3d_cross_attn_fwd(q, k, v, mask=m, save_for_backward=True)
+    g = p3d().pack3d_cross_attn_bwd(q, k, v, f, dO, mask=m)
+    bad = torch.zeros(3, 4, N, dtype=torch.bool, device="cuda")  # rows touched
+    bad[0, 1, N // 2] = bad[1, 2, N - 1] = bad[1, 0, 0] = True
+    q2, dO2 = q.clone(), dO.clone()
+    dO2[0, 1, N // 2, 5] = math.inf
+    dO2[1, 2, N - 1, d - 1] = -math.inf
+    q2[1, 0, 0, 3] = math.nan
+    f2 = p3d().pack3d_cross_attn_fwd(q2, k, v, mask=m, save_for_backward=True)
+    g2 = p3d().pack3d_cross_attn_bwd(q2, k, v, f2, dO2, mask=m)
+    off = ~m[:, None, :, None].expand_as(k)
+    for n in ("dk", "dv"):
+        assert bool((g2[n][off] == 0).all()), n
+        assert torch.equal(g2[n][2], g[n][2]), n
+        assert torch.equal(g2[n][0, 1], g[n][0, 1]), n  # the other KV head of the entry
+    none = (~m.any(1))[:, None, None, None].expand_as(q)
+    assert bool((g2["dq"][none] == 0).all()) and bool((f2["o"][none] == 0).all())
+    assert torch.equal(g2["dq"][~bad], g["dq"][~bad])
