@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(bwd_threads(GT))
 }
 
 // Rows longer than a block's registers hold: one block per row, which is read once per pass (the
-// later passes hit L1 / L2).
+// later passes hit L1 / L2). Columns are counted in 64 bits here: up to 2^31 - 1 of them, a counter
+// runs a block's threads past the last.
 constexpr int kLongThreads = 512;
 template <int K> __device__ __forceinline__ void block_sum(float (&v)[K], float* red) {
   __syncthreads();  // the previous sum's words have been read
@@ -334,19 +335,19 @@ __global__ void __launch_bounds__(kLongThreads)
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const T* xr = x + row * cols;
     float s[1] = {0.f};
-    for (int c = threadIdx.x; c < cols; c += kLongThreads) s[0] += to_f(xr[c]);
+    for (int64_t c = threadIdx.x; c < cols; c += kLongThreads) s[0] += to_f(xr[c]);
     block_sum(s, red);
     const float mu = s[0] / (float)cols;
     s[0] = 0.f;
-    for (int c = threadIdx.x; c < cols; c += kLongThreads) {
+    for (int64_t c = threadIdx.x; c < cols; c += kLongThreads) {
       const float d = to_f(xr[c]) - mu;
       s[0] = fmaf(d, d, s[0]);
     }
     block_sum(s, red);
     const float rs = 1.f / sqrtf(s[0] / (float)cols + eps);
-    for (int c = threadIdx.x; c < cols; c += kLongThreads)
-      y[row * cols + c] = from_f<T>(fmaf((to_f(xr[c]) - mu) * rs, param(w, wtype, c, 1.f),
-                                         param(b, wtype, c, 0.f)));
+    for (int64_t c = threadIdx.x; c < cols; c += kLongThreads)
+      y[row * cols + c] = from_f<T>(fmaf((to_f(xr[c]) - mu) * rs, param(w, wtype, (int)c, 1.f),
+                                         param(b, wtype, (int)c, 0.f)));
     if (threadIdx.x == 0) {
       if (mean) mean[row] = mu;
       if (rstd) rstd[row] = rs;
@@ -365,15 +366,15 @@ __global__ void __launch_bounds__(kLongThreads)
     const T* dr = dy + row * cols;
     const float mu = mean[row], rs = rstd[row];
     float s[2] = {0.f, 0.f};
-    for (int c = threadIdx.x; c < cols; c += kLongThreads) {
-      const float g = to_f(dr[c]) * param(w, wtype, c, 1.f);
+    for (int64_t c = threadIdx.x; c < cols; c += kLongThreads) {
+      const float g = to_f(dr[c]) * param(w, wtype, (int)c, 1.f);
       s[0] += g;
       s[1] = fmaf(g, (to_f(xr[c]) - mu) * rs, s[1]);
     }
     block_sum(s, red);
     const float mg = s[0] / (float)cols, mgx = s[1] / (float)cols;
-    for (int c = threadIdx.x; c < cols; c += kLongThreads) {
-      const float g = to_f(dr[c]) * param(w, wtype, c, 1.f);
+    for (int64_t c = threadIdx.x; c < cols; c += kLongThreads) {
+      const float g = to_f(dr[c]) * param(w, wtype, (int)c, 1.f);
       dx[row * cols + c] = from_f<T>(rs * (g - mg - (to_f(xr[c]) - mu) * rs * mgx));
     }
   }
@@ -384,7 +385,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     k_ln_cols(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ mean,
               const float* __restrict__ rstd, int64_t rows, int cols, float* __restrict__ part) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
+  const int64_t c = blockIdx.x * 256ll + threadIdx.x;
   if (c >= cols) return;
   float a = 0.f, b = 0.f;
   for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(1024)
                 void* __restrict__ dw, void* __restrict__ db) {
   __shared__ float acc[32][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int64_t c = blockIdx.x * 32ll + lane;
   void* dst = blockIdx.y ? db : dw;
   if (!dst) return;
   float s = 0.f;
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(1024)
   float r = acc[lane][g];  // warp g adds column g
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-  const int col = blockIdx.x * 32 + g;
+  const int64_t col = blockIdx.x * 32ll + g;
   if (lane == 0 && col < cols) {
     if (wtype == PACK3D_BF16)
       static_cast<__nv_bfloat16*>(dst)[col] = __float2bfloat16_rn(r);
@@ -530,7 +531,7 @@ template <typename T> int launch(const Args& a, bool bwd) {
   int parts = 0;
   if (a.part) {
     parts = (int)(a.rows < 64 ? a.rows : 64);
-    k_ln_cols<T><<<dim3((a.cols + 255) / 256, parts), 256, 0, a.s>>>(
+    k_ln_cols<T><<<dim3((unsigned)((a.cols + 255ll) / 256), parts), 256, 0, a.s>>>(
         static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.cmean, a.crstd, a.rows, a.cols,
         a.part);
     count_launch();
@@ -617,7 +618,7 @@ extern "C" pack3d_status pack3d_layer_norm_bwd(const void* dy, const void* x, co
     count_launch();
   }
   if (cols_out) {  // no rows: the sums are zero
-    ln::k_ln_finish<<<dim3((cols + 31) / 32, 2), 1024, 0, a.s>>>(a.part, parts, cols, wdtype,
+    ln::k_ln_finish<<<dim3((unsigned)((cols + 31ll) / 32), 2), 1024, 0, a.s>>>(a.part, parts, cols, wdtype,
                                                                dweight, dbias);
     count_launch();
   }

@@ -127,3 +127,30 @@ def test_gradient_against_differences():
 @pytest.mark.parametrize("rows,cols", [(30001, 3), (20001, 9), (9001, 31), (5001, 333), (3001, 511), (1, 257)])
 def test_ragged_widths_over_many_rows(dtype, rows, cols):
     run_and_check(*make(rows, cols, dtype, torch.float32))
+
+
+def test_the_longest_row():
+    # 2^31 - 1 columns: the last ones lie less than a block's threads below the largest 32-bit number.
+    # Of a row of +1, -1, +1, ... every partial sum is a whole number below 2^24 until 512 of them
+    # are added, so the mean is 2^-31 to within rounding, and the variance 1.
+    cols = 2 ** 31 - 1
+    x = torch.ones(1, cols, dtype=torch.bfloat16, device="cuda")
+    x[0, 1::2] = -1
+    f = p3d().pack3d_layer_norm_fwd(x, save_for_backward=True)
+    assert torch.equal(f["y"], x)  # (1 +- 2^-31) / sqrt(1 + 1e-5), rounded
+    assert abs(float(f["mean"])) <= 2.0 ** -24 and abs(float(f["rstd"]) - (1 + 1e-5) ** -0.5) <= 8 * ob.U
+    del f["y"]
+    g = p3d().pack3d_layer_norm_bwd(x, x, None, f)
+    rstd = float(f["rstd"])
+    for at in (slice(0, 1000), slice(cols - 1000, cols)):
+        assert bool(((g["dweight"][at] - rstd).abs() <= 2.0 ** -22).all())
+        assert torch.equal(g["dbias"][at], x[0, at].float())
+        # dx = rstd (g - mean g - x^ mean(g x^)) with g = x and x^ = rstd x, so x dx is
+        # rstd (1 - rstd mean(rstd)) = 1e-5. A thread adds 2^22 terms rstd = 1 - 5e-6 to a float32 sum,
+        # whose steps from 2^8 on are 2^-15 and more: there each term counts as 1. The mean lies between
+        # rstd and 1, and x dx between rstd (1 - rstd) = 5e-6 and 1e-5, to within a few roundings of
+        # terms of size one.
+        xdx = g["dx"][0, at].float() * x[0, at].float()
+        low, high = float(xdx.min()), float(xdx.max())
+        assert rstd * (1 - rstd) - 2.0 ** -20 <= low and high <= 1e-5 + 2.0 ** -20
+    assert float(g["dweight"].min()) > 0.99 and float(g["dweight"].max()) < 1.01
