@@ -446,6 +446,13 @@ def _need(t, what, shape, dtype, index):
         raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
 
 
+def _int32(n, what):
+    """n as the ABI's 32-bit integer: ctypes would wrap a larger one to another size."""
+    if n >= 1 << 31:
+        raise ValueError(f"{what} is {n}, expected less than 2^31")
+    return n
+
+
 def _code(t):
     code = _CODES.get(t.dtype)
     return _dtype_code(t) if code is None else code  # raises for other types
@@ -486,6 +493,7 @@ def _cross_shapes(q, k, v, mask):
     _need(v, "v", k_shape, dt, index)
     if HK == 0:
         raise ValueError("k has no heads")
+    _int32(max(B, H, HK, d), "the largest of batch, heads and head_dim")
     if mask is not None:
         if mask.dtype != torch.bool and mask.dtype != torch.uint8:
             raise TypeError(f"mask is {mask.dtype}, expected torch.bool or torch.uint8")
@@ -589,12 +597,12 @@ def pack3d_layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None,
     code, index, shape = _code(x), x.get_device(), x.shape
     if not shape or shape[-1] < 1:
         raise ValueError("x needs a last dimension of one or more elements")
+    cols = _int32(shape[-1], "the last dimension of x")
     _need(x, "x", None, x.dtype, index)
     if not _here(x):
         with torch.cuda.device(x.device):
             return pack3d_layer_norm_fwd(x, weight, bias, eps=eps, y=y,
                                          save_for_backward=save_for_backward, stream=stream)
-    cols = shape[-1]
     rows = x.numel() // cols
     wtype = _norm_params(cols, index, weight, bias)
     if y is None:
@@ -622,12 +630,12 @@ def pack3d_layer_norm_bwd(dy, x, weight, saved, *, weight_grad=True, bias_grad=T
     code, index, shape = _code(x), x.get_device(), x.shape
     if not shape or shape[-1] < 1:
         raise ValueError("x needs a last dimension of one or more elements")
+    cols = _int32(shape[-1], "the last dimension of x")
     _need(x, "x", None, x.dtype, index)
     if not _here(x):
         with torch.cuda.device(x.device):
             return pack3d_layer_norm_bwd(dy, x, weight, saved, weight_grad=weight_grad,
                                          bias_grad=bias_grad, workspace=workspace, stream=stream)
-    cols = shape[-1]
     rows = x.numel() // cols
     wtype = _norm_params(cols, index, weight)
     mean, rstd = saved["mean"], saved["rstd"]

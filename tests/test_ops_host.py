@@ -203,3 +203,33 @@ def test_list_helper_refuses_what_is_no_dense_tensor_of_the_device():
     with pytest.raises(TypeError):
         b._tensor_list([t, None][1:], "grads", 0)
     assert b._tensor_list([], "grads", 0) == (b"", b"", b"")
+
+
+class Shaped:
+    """A CUDA tensor of a shape, as far as the binding's checks look."""
+
+    is_cuda, dtype = True, torch.bfloat16
+
+    def __init__(self, *shape):
+        self.shape = torch.Size(shape)
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+
+def test_binding_refuses_sizes_that_the_abi_would_wrap():
+    # 2^32 + 96 would reach the library as 96
+    big = (1 << 32) + 96
+    x = Shaped(1, 2, 3, big)
+    for call in (lambda: b.pack3d_cross_attn_fwd(x, x, x), lambda: b.pack3d_layer_norm_fwd(x),
+                 lambda: b.pack3d_layer_norm_bwd(x, x, None, {}),
+                 lambda: b._cross_shapes(Shaped(1, big, 0, 96), *[Shaped(1, 2, 3, 96)] * 2, None)):
+        with pytest.raises(ValueError, match="less than 2\\^31"):
+            call()
+    assert b._cross_shapes(*[Shaped(1, 2, 3, 96)] * 3, None)[:6] == (1, 2, 2, 3, 3, 96)
