@@ -489,10 +489,15 @@ template <typename T, int GT, int E> int by_pieces(const Args& a, bool bwd, int 
 // 650 us, by 32 308; 1,000,000 x 7 by 8 threads of 8 elements 127 us, by 4 of 2 47).
 constexpr int kGroups[7] = {4, 8, 16, 32, 128, 256, 512};
 constexpr int kSingles = 8;
+// Rows of whole pieces of e elements move by pieces as far as registers hold them; ragged and longer
+// rows move by elements and may start at any.
+constexpr bool moves_by_pieces(int cols, int e) {
+  return cols % e == 0 && cols / e <= 4 * kGroups[6];
+}
 
 template <typename T> int launch(const Args& a, bool bwd) {
   constexpr int E = 16 / (int)sizeof(T);
-  if (a.cols % E == 0) {
+  if (moves_by_pieces(a.cols, E)) {
     const int pieces = a.cols / E;
     for (int gt : kGroups) {
       const int nv = (pieces + gt - 1) / gt;
@@ -541,6 +546,12 @@ template <typename T> int launch(const Args& a, bool bwd) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+bool aligned_rows(const void* p, int dtype, int cols) {
+  const int size = dtype == PACK3D_BF16 ? 2 : 4;
+  const int by = moves_by_pieces(cols, 16 / size) ? 16 : size;
+  return reinterpret_cast<uintptr_t>(p) % by == 0;
+}
+
 pack3d_status check(int dtype, int wtype, int64_t rows, int32_t cols) {
   if ((dtype != PACK3D_F32 && dtype != PACK3D_BF16) || (wtype != PACK3D_F32 && wtype != PACK3D_BF16))
     return PACK3D_ERR_INVALID_ARG;
@@ -567,7 +578,8 @@ extern "C" pack3d_status pack3d_layer_norm_fwd(const void* x, const void* weight
   if (!(eps >= 0.f) || isinf(eps)) return PACK3D_ERR_INVALID_ARG;
   if (rows == 0) return PACK3D_OK;
   if (!x || !y) return PACK3D_ERR_INVALID_ARG;
-  if (!ln::aligned16(x) || !ln::aligned16(y)) return PACK3D_ERR_ALIGN;
+  if (!ln::aligned_rows(x, dtype, cols) || !ln::aligned_rows(y, dtype, cols))
+    return PACK3D_ERR_ALIGN;
   if (x == y) return PACK3D_ERR_INVALID_ARG;  // a row is fetched ahead of the stores before it
   ln::Args a{};
   a.x = x; a.w = weight; a.b = bias; a.y = y; a.mean = mean; a.rstd = rstd;
@@ -598,7 +610,8 @@ extern "C" pack3d_status pack3d_layer_norm_bwd(const void* dy, const void* x, co
   const bool cols_out = dweight || dbias;
   if (rows > 0) {
     if (!dy || !x || !mean || !rstd || !dx) return PACK3D_ERR_INVALID_ARG;
-    if (!ln::aligned16(dy) || !ln::aligned16(x) || !ln::aligned16(dx)) return PACK3D_ERR_ALIGN;
+    for (const void* p : {dy, x, static_cast<const void*>(dx)})
+      if (!ln::aligned_rows(p, dtype, cols)) return PACK3D_ERR_ALIGN;
     if (dx == dy || dx == x) return PACK3D_ERR_INVALID_ARG;
     if (cols_out) {
       if (!workspace) return PACK3D_ERR_INVALID_ARG;

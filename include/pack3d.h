@@ -326,7 +326,8 @@ pack3d_status pack3d_read_status(int32_t* status, void* stream);
 /* Layer norm over the last dimension: y = (x - mu) / sqrt(var + eps) * weight + bias, mu and var
  * the mean and (biased) variance of the row in float32.
  * x, y          device [rows, cols] dtype, rows 0 or more, cols 1 or more (any length: a [B, H, N,
- *               d] tensor is B H N rows of d).
+ *               d] tensor is B H N rows of d). Rows that are no whole number of 16-byte pieces, or
+ *               longer than 2,048 of them, need element alignment only.
  * weight, bias  device [cols] of wdtype (element-aligned), or NULL for 1 and 0.
  * eps           0 or more, finite.
  * mean, rstd    device float32 [rows] or NULL: mu and 1 / sqrt(var + eps), what the backward

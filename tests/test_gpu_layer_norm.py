@@ -154,3 +154,21 @@ def test_the_longest_row():
         low, high = float(xdx.min()), float(xdx.max())
         assert rstd * (1 - rstd) - 2.0 ** -20 <= low and high <= 1e-5 + 2.0 ** -20
     assert float(g["dweight"].min()) > 0.99 and float(g["dweight"].max()) < 1.01
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [1, 7, 31, 333, 1001, 8191, 8201, 17001])
+def test_ragged_rows_start_at_any_element(dtype, cols):
+    # a slice of rows of an odd width starts where the row before it ends
+    x, w, b, dy = make(12, cols, dtype, torch.float32, seed=6)
+    want, wantg = run_and_check(x[1:].clone(), w, b, dy[1:].clone())
+    for shift in (1, 3):
+        buf, out = (torch.full((11 * cols + 16,), 5.0, dtype=dtype, device="cuda") for _ in range(2))
+        view, y = (t[shift:shift + 11 * cols].view(11, cols) for t in (buf, out))
+        view.copy_(x[1:])
+        f = p3d().pack3d_layer_norm_fwd(view, w, b, y=y, save_for_backward=True)
+        assert torch.equal(y, want["y"]) and f["y"] is y
+        assert bool((out[:shift] == 5.0).all()) and bool((out[shift + 11 * cols:] == 5.0).all())
+        g = p3d().pack3d_layer_norm_bwd(dy[1:], view, w, f)
+        for n in ("dx", "dweight", "dbias"):
+            assert torch.equal(g[n], wantg[n]), n

@@ -233,3 +233,17 @@ def test_binding_refuses_sizes_that_the_abi_would_wrap():
         with pytest.raises(ValueError, match="less than 2\\^31"):
             call()
     assert b._cross_shapes(*[Shaped(1, 2, 3, 96)] * 3, None)[:6] == (1, 2, 2, 3, 3, 96)
+
+
+@pytest.mark.parametrize("dtype,cols,at,status", [
+    (1, 8, 2, 5), (1, 16384, 2, 5), (0, 4, 4, 5), (0, 8192, 4, 5),  # whole pieces: 16 bytes
+    (1, 333, 1, 5), (1, 16392, 1, 5), (0, 333, 2, 5), (0, 8196, 2, 5)])  # otherwise: an element
+def test_layer_norm_alignment_by_the_rows_length(dtype, cols, at, status):
+    for off in ((at, 0, 0), (0, at, 0), (0, 0, at)):
+        x, dy, y = FAKE + off[0], 2 * FAKE + off[1], 3 * FAKE + off[2]
+        if off[1] == 0:
+            assert b.lib().pack3d_layer_norm_fwd(x, None, None, dtype, 0, 1, cols, 1e-5, y, None, None,
+                                                 None) == status
+        assert b.lib().pack3d_layer_norm_bwd(dy, x, None, FAKE, FAKE, dtype, 0, 1, cols, y, None, None, None, 0,
+                                             None) == status
+        assert b.lib().pack3d_last_launch_count() == 0
