@@ -670,7 +670,8 @@ def _tensor_list(ts, what, index):
     """Lengths, type codes and addresses of a list of tensors as bytes, each tensor checked."""
     global _list_module
     if _list_module is None:
-        path = os.path.join(os.path.dirname(_LIB_PATH), "_tensor_list.so")
+        from .build import tensor_list_path
+        path = tensor_list_path()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} not found: run python -m geometry_aware_local_pack3d_b200.build")
         spec = importlib.util.spec_from_file_location("_tensor_list", path)

@@ -1,5 +1,6 @@
-"""Build step: compile the CUDA sources of the package into lib/libpack3d.so for sm_100a, and the
-binding's helper for lists of tensors into lib/_tensor_list.so.
+"""Build step: compile the CUDA sources of the package into lib/libpack3d.so for sm_100a, then the
+binding's helper for lists of tensors into lib/ (tensor_list_path). The library needs nvcc alone; where
+the helper cannot be built, that is a warning, and the calls over lists of tensors say so when used.
 
 Usage: python -m geometry_aware_local_pack3d_b200.build [--force] [--verbose]
 Objects go to _build/ (git-ignored); the shared library is written in-tree so it travels
@@ -14,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,7 +24,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "lib", "libpack3d.so")
 LIST_SRC = os.path.join(CSRC, "tensor_list.cpp")
-LIST_LIB = os.path.join(PKG, "lib", "_tensor_list.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3",
@@ -57,14 +58,25 @@ def _compile(src, verbose, extra):
     return obj, r.stderr
 
 
+def tensor_list_path():
+    """The helper's file: it is compiled against torch's classes and Python's ABI, so both versions
+    are in its name, and one that was built for others is not found."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    key = f"torch{torch.__version__}-cxx{abi}-{sysconfig.get_config_var('SOABI')}"
+    return os.path.join(PKG, "lib", f"_tensor_list-{key}.so")
+
+
 def build_tensor_list(force=False):
     """The host helper that reads a list of tensors (a CPython module over torch's headers)."""
+    out = tensor_list_path()
     newest = max(os.path.getmtime(LIST_SRC), os.path.getmtime(__file__))
-    if not force and os.path.exists(LIST_LIB) and os.path.getmtime(LIST_LIB) >= newest:
-        return LIST_LIB
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= newest:
+        return out
     import torch
+    os.makedirs(os.path.dirname(out), exist_ok=True)
     root = os.path.dirname(torch.__file__)
-    tmp = LIST_LIB + ".tmp"
+    tmp = out + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(root, "include"),
@@ -74,14 +86,22 @@ def build_tensor_list(force=False):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {LIST_SRC}:\n{r.stderr}")
-    os.replace(tmp, LIST_LIB)
-    return LIST_LIB
+    os.replace(tmp, out)
+    return out
 
 
 def build(force=False, verbose=False, extra=()):
+    lib = build_library(force, verbose, extra)
+    try:
+        build_tensor_list(force)
+    except (RuntimeError, OSError, ImportError) as e:
+        warnings.warn(f"the helper for lists of tensors was not built: {e}")
+    return lib
+
+
+def build_library(force=False, verbose=False, extra=()):
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
-    build_tensor_list(force)
     srcs = sources()
     newest = max(os.path.getmtime(p) for p in srcs + headers() + [__file__])
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:

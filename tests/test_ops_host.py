@@ -247,3 +247,32 @@ def test_layer_norm_alignment_by_the_rows_length(dtype, cols, at, status):
         assert b.lib().pack3d_layer_norm_bwd(dy, x, None, FAKE, FAKE, dtype, 0, 1, cols, y, None, None, None, 0,
                                              None) == status
         assert b.lib().pack3d_last_launch_count() == 0
+
+
+def test_the_library_is_built_without_the_list_helper(monkeypatch, tmp_path):
+    from geometry_aware_local_pack3d_b200 import build as bd
+    steps = []
+
+    def no_compiler(*a, **k):
+        steps.append("helper")
+        raise FileNotFoundError("g++")
+
+    monkeypatch.setattr(bd, "build_library", lambda *a: steps.append("library") or bd.LIB)
+    monkeypatch.setattr(bd, "tensor_list_path", lambda: str(tmp_path / "none.so"))
+    monkeypatch.setattr(bd.subprocess, "run", no_compiler)
+    with pytest.warns(UserWarning, match="lists of tensors"):
+        assert bd.build() == bd.LIB
+    assert steps == ["library", "helper"]
+    # the calls over lists of tensors then say what is missing
+    monkeypatch.setattr(b, "_list_module", None)
+    with pytest.raises(RuntimeError, match="none.so not found"):
+        b._tensor_list([], "grads", 0)
+
+
+def test_the_list_helper_of_another_torch_or_python_is_not_taken(monkeypatch):
+    from geometry_aware_local_pack3d_b200 import build as bd
+    here = bd.tensor_list_path()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    other_torch = bd.tensor_list_path()
+    monkeypatch.setattr(bd.sysconfig, "get_config_var", lambda n: "cpython-1")
+    assert len({here, other_torch, bd.tensor_list_path()}) == 3
