@@ -835,13 +835,14 @@ static cudaError_t launch_bwd(const Problem& p, const MaskTables& m, const void*
     e = smem_attr_once(reinterpret_cast<const void*>(k_cross_dkv<D>), Sk::kBytes, ak);
   if (e != cudaSuccess) return e;
   // the split of registers needs every one of the launch's
-  static const bool split_fits = [] {
-    cudaFuncAttributes a, b;
-    return cudaFuncGetAttributes(&a, k_cross_dq<D>) == cudaSuccess &&
-           cudaFuncGetAttributes(&b, k_cross_dkv<D>) == cudaSuccess && a.numRegs >= xq::kRegs &&
-           b.numRegs >= xk::kRegs;
-  }();
-  if (!split_fits) return cudaErrorLaunchOutOfResources;
+  static PerDevice split_fits;
+  if (!split_fits.get([] {
+        cudaFuncAttributes a, b;
+        return cudaFuncGetAttributes(&a, k_cross_dq<D>) == cudaSuccess &&
+               cudaFuncGetAttributes(&b, k_cross_dkv<D>) == cudaSuccess && a.numRegs >= xq::kRegs &&
+               b.numRegs >= xk::kRegs;
+      }))
+    return cudaErrorLaunchOutOfResources;
   CUtensorMap q128, g128, k64, v64, o128, q64, g64, k128, v128;
   if (!encode_rows<D>(&q128, p.q, p.np, p.bh, kTile) ||
       !encode_rows<D>(&g128, dO, p.np, p.bh, kTile) ||

@@ -821,11 +821,12 @@ static cudaError_t launch_fwd(const Problem& p, const MaskTables& m, void* o, fl
   cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(k_cross_fwd<D>), S::kBytes, attr);
   if (e != cudaSuccess) return e;
   // a split of more registers than the block was launched with would wait for ever
-  static const bool split_fits = [] {
-    cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, k_cross_fwd<D>) == cudaSuccess && a.numRegs >= xf::kRegs;
-  }();
-  if (!split_fits) return cudaErrorLaunchOutOfResources;
+  static PerDevice split_fits;
+  if (!split_fits.get([] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, k_cross_fwd<D>) == cudaSuccess && a.numRegs >= xf::kRegs;
+      }))
+    return cudaErrorLaunchOutOfResources;
   CUtensorMap mq, mk, mv, mo;
   if (!encode_rows<D>(&mq, p.q, p.np, p.bh, kTile) || !encode_rows<D>(&mk, p.k, p.l, p.bh, S::KT) ||
       !encode_rows<D>(&mv, p.v, p.l, p.bh, S::KT) || !encode_rows<D>(&mo, o, p.np, p.bh, kTile))

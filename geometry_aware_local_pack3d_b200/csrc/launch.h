@@ -30,6 +30,26 @@ inline int sm_count() {
   return v;
 }
 
+// A number that belongs to a kernel on a device (its blocks there, say): look() is asked once per
+// device. An answer of 0 or less (a failed look) is not kept, nor is one of a device beyond the cache.
+class PerDevice {
+ public:
+  template <typename F> int get(F look) {
+    int dev = 0;
+    const bool cacheable = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxCachedDevices;
+    if (cacheable) {
+      const int c = cache_[dev].load(std::memory_order_relaxed);
+      if (c > 0) return c;
+    }
+    const int v = look();
+    if (cacheable && v > 0) cache_[dev].store(v, std::memory_order_relaxed);
+    return v;
+  }
+
+ private:
+  std::atomic<int> cache_[kMaxCachedDevices] = {};
+};
+
 // Cycle budget of every bounded device-side wait of the tensor-core kernels, read at each
 // launch. The default (4e9 SM cycles, about 2 s at 1.97 GHz) is far above any legitimate wait;
 // pack3d_testing_set_wait_budget lowers it so that a test can make a wait run out.

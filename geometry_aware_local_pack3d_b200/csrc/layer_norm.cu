@@ -440,12 +440,14 @@ struct Args {
 };
 
 // Blocks that fill the device: the launch's blocks are persistent.
-inline int grid_for(const void* fn, int threads, int64_t blocks) {
-  int per = 1;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, 0) != cudaSuccess || per < 1)
-    per = 1;
-  const int64_t cap = (int64_t)per * sm_count();
-  return (int)(blocks < cap ? blocks : cap);
+inline int grid_for(const void* fn, int threads, PerDevice& cache) {
+  const int n = cache.get([&] {
+    int per = 0;
+    const bool ok =
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, 0) == cudaSuccess;
+    return ok ? per * sm_count() : 0;
+  });
+  return n > 0 ? n : sm_count();
 }
 
 constexpr int kMaxParts = 2048;  // most blocks a backward launch may have (a row of sums each)
@@ -454,8 +456,8 @@ template <typename T, int GT, int NV, int E> int run(const Args& a, bool bwd) {
   constexpr int BT = block_threads(GT), GROUPS = BT / GT;
   const int64_t blocks = (a.rows + GROUPS - 1) / GROUPS;
   if (!bwd) {
-    static const int cap = grid_for(reinterpret_cast<const void*>(k_ln_fwd<T, GT, NV, E>), BT,
-                                    INT64_MAX);
+    static PerDevice fit;
+    const int cap = grid_for(reinterpret_cast<const void*>(k_ln_fwd<T, GT, NV, E>), BT, fit);
     const int grid = (int)(blocks < cap ? blocks : cap);
     k_ln_fwd<T, GT, NV, E><<<grid, BT, 0, a.s>>>(
         static_cast<const T*>(a.x), a.w, a.b, a.wtype, a.rows, a.cols, a.eps,
@@ -464,8 +466,9 @@ template <typename T, int GT, int NV, int E> int run(const Args& a, bool bwd) {
   }
   constexpr int BB = bwd_threads(GT);
   const int64_t bblocks = (a.rows + BB / GT - 1) / (BB / GT);
-  static const int cap = grid_for(reinterpret_cast<const void*>(k_ln_bwd<T, GT, NV, E>), BB,
-                                  kMaxParts);
+  static PerDevice fit;
+  const int most = grid_for(reinterpret_cast<const void*>(k_ln_bwd<T, GT, NV, E>), BB, fit);
+  const int cap = most < kMaxParts ? most : kMaxParts;
   const int grid = (int)(bblocks < cap ? bblocks : cap);
   k_ln_bwd<T, GT, NV, E><<<grid, BB, 0, a.s>>>(
       static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.w, a.wtype, a.cmean, a.crstd,

@@ -276,3 +276,48 @@ def test_the_list_helper_of_another_torch_or_python_is_not_taken(monkeypatch):
     other_torch = bd.tensor_list_path()
     monkeypatch.setattr(bd.sysconfig, "get_config_var", lambda n: "cpython-1")
     assert len({here, other_torch, bd.tensor_list_path()}) == 3
+
+
+FAKE_RUNTIME = """
+#include "launch.h"
+static int device = 0, looks = 0;
+thread_local int p3d::g_launches = 0;
+extern "C" {
+cudaError_t cudaGetDevice(int* d) { *d = device; return cudaSuccess; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) { *v = 148; return cudaSuccess; }
+cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { return cudaSuccess; }
+int look_on(int d, int answer) {
+  static p3d::PerDevice cache;
+  device = d;
+  return cache.get([&] { ++looks; return answer; });
+}
+int looks_so_far(void) { return looks; }
+}
+"""
+
+
+def test_what_a_launch_keeps_is_kept_per_device(tmp_path):
+    import shutil
+    import subprocess
+
+    from geometry_aware_local_pack3d_b200 import build as bd
+    (tmp_path / "fake.cpp").write_text(FAKE_RUNTIME)
+    cuda = bd.os.path.join(bd.os.path.dirname(bd.os.path.dirname(bd.os.path.realpath(bd.nvcc()))), "include")
+    out = str(tmp_path / "fake.so")
+    subprocess.run([shutil.which("g++") or "g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", cuda,
+                    "-I", bd.CSRC, str(tmp_path / "fake.cpp"), "-o", out], check=True)
+    fake = ctypes.CDLL(out)
+    assert [fake.look_on(0, 296), fake.look_on(1, 264), fake.look_on(0, 7), fake.look_on(1, 7)] == \
+        [296, 264, 296, 264] and fake.looks_so_far() == 2
+    # a failed look is asked again, and so is a device beyond the cache
+    assert [fake.look_on(2, 0), fake.look_on(2, 5), fake.look_on(2, 6)] == [0, 5, 5]
+    assert [fake.look_on(64, 8), fake.look_on(64, 9)] == [8, 9]
+
+
+def test_no_launch_keeps_a_device_number_per_process():
+    import re
+
+    from geometry_aware_local_pack3d_b200 import build as bd
+    for path in bd.sources():
+        text = open(path).read()
+        assert not re.search(r"static const (int|bool) \w+ = (grid_for|\[\])", text), path
