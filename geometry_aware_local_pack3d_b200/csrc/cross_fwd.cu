@@ -24,8 +24,6 @@
 // Masked states: their S is replaced by -inf whatever it holds, and their V rows (which may hold
 // NaN) are zeroed in shared memory, in the tiles that mix masked and unmasked states; tiles without
 // an unmasked state are not in the list and are never loaded.
-// A context of one tile stays in shared memory while its problem lasts: the CTAs then take runs of
-// consecutive units, and only the rows move.
 // When there are fewer units than SMs and several state tiles, the states are split over nsplit
 // CTAs; each writes its normalised fp32 rows and lse, and k_cross_join adds them with the weights
 // exp(lse_s - lse).
@@ -84,28 +82,20 @@ struct Params {
   int64_t np, l, bh, words;
   int units, pairs, tiles, kv_heads, nsplit;
   int step_pr, step_bh;  // pairs and problems from one unit of a CTA to its next
-  int resident;      // one state tile: K and V stay while the problem lasts
   float scale_log2;
 };
 
-// The units of a CTA in order: every gridDim-th, or a run of consecutive ones. A unit is a pair of
-// row tiles of one problem, with its range [j0, j1) of the batch entry's list of state tiles.
+// The units of a CTA in order: every gridDim-th. A unit is a pair of row tiles of one problem, with its
+// range [j0, j1) of the batch entry's list of state tiles. A problem has two state tiles or more:
+// shorter contexts have a kernel of their own.
 struct Units {
   int left;              // units still to come, this one included
   int bh, pr, split, j0, j1;
   const int32_t* list;   // null: tile j is j
   const uint32_t* bits;
-  bool fresh;            // the problem's first unit here
   __device__ __forceinline__ explicit Units(const Params& P) {
-    const uint32_t b = blockIdx.x, g = gridDim.x, n = P.units;
-    uint32_t first = b;
-    if (P.resident) {
-      const uint32_t per = n / g, more = n - per * g;
-      first = b * per + min(b, more);
-      left = (int)(per + (b < more ? 1 : 0));
-    } else {
-      left = (int)((n - b + g - 1) / g);
-    }
+    uint32_t first = blockIdx.x;
+    left = (int)(((uint32_t)P.units - first + gridDim.x - 1) / gridDim.x);
     split = 0;
     if (P.nsplit > 1) {  // (the units are then at most the CTAs: one each)
       split = (int)(first % (uint32_t)P.nsplit);
@@ -113,7 +103,6 @@ struct Units {
     }
     bh = (int)(first / (uint32_t)P.pairs);
     pr = (int)(first - (uint32_t)bh * P.pairs);
-    fresh = true;
     place(P);
   }
   __device__ __forceinline__ void place(const Params& P) {
@@ -143,17 +132,11 @@ struct Units {
       pr -= P.pairs;
       ++bh;
     }
-    fresh = bh != was;
-    if (P.act && fresh) place(P);
+    if (P.act && bh != was) place(P);
   }
   __device__ __forceinline__ bool any() const { return j0 != j1; }
   __device__ __forceinline__ int64_t row0() const { return (int64_t)pr * (2 * kTile); }
   __device__ __forceinline__ bool two(const Params& P) const { return row0() + kTile < P.np; }
-  // the unit's state tiles are loaded for it, and given back after it
-  __device__ __forceinline__ bool loads(const Params& P) const { return !P.resident || fresh; }
-  __device__ __forceinline__ bool releases(const Params& P) const {
-    return !P.resident || left == 1 || pr + 1 == P.pairs;
-  }
   __device__ __forceinline__ int tile(int j) const { return list ? list[j] : j; }
 };
 }  // namespace xf
@@ -464,7 +447,6 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
                          &bars[B_QFULL + i]);
             if (t) ++uc[1]; else ++uc[0];
           }
-          if (!U.loads(P)) continue;
 #pragma unroll 1
           for (int j = 2 * U.j0; j < 2 * U.j1 && ok; ++j, ++kv) {
             // K and V of a tile take turns
@@ -491,12 +473,12 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
       const uint32_t id_s = tc::idesc_bf16_f32(128, KT, false, false);
       const uint64_t qd0 = Ly::kdesc(tc::smem_u32(smem + S::kQ + t * S::QB));
       const uint64_t kd0 = Ly::kdesc(tc::smem_u32(smem + S::kRing));
-      uint32_t kv = 0, n = 0, uc = 0;  // slot pairs given back; state tiles and units so far
+      uint32_t kv = 0, n = 0, uc = 0;  // state tiles; those and the units of this row tile
       bool ok = true;
 #pragma unroll 1
       for (Units U(P); U.left > 0 && ok; U.next(P)) {
         if (!U.any()) continue;
-        const bool mine = t == 0 || U.two(P), gives = U.releases(P);
+        const bool mine = t == 0 || U.two(P);
         if (mine) ok = ab.all(sb + 8 * (B_QFULL + 2 * (uc & 1) + t), uc >> 1);
         const uint64_t qd = qd0 + ((2 * (uc & 1) * S::QB) >> 4);
 #pragma unroll 1
@@ -518,11 +500,11 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
                            ks > 0);
               commit32(sb + 8 * (B_SFULL + 2 * b + t));
             }
-            if (gives) commit32(sb + 8 * (B_EMPTY + st));
+            commit32(sb + 8 * (B_EMPTY + st));
           }
           __syncwarp();
           n += mine;
-          kv += gives;
+          ++kv;
         }
         uc += mine;
       }
@@ -542,7 +524,7 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
 #pragma unroll 1
       for (Units U(P); U.left > 0 && ok; U.next(P)) {
         if (!U.any()) continue;
-        const bool mine = t == 0 || U.two(P), gives = U.releases(P);
+        const bool mine = t == 0 || U.two(P);
         // O still holds the previous unit's rows until the epilogue has read them
         if (mine && uc) ok = ab.all(sb + 8 * (B_OFREE + t), uc - 1);
 #pragma unroll 1
@@ -564,11 +546,11 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
               commit32(sb + 8 * (B_DONE + t));
               if (j + 1 == U.j1) commit32(sb + 8 * (B_OFULL + t));
             }
-            if (gives) commit32(sb + 8 * (B_EMPTY + st));
+            commit32(sb + 8 * (B_EMPTY + st));
           }
           __syncwarp();
           n += mine;
-          kv += gives;
+          ++kv;
         }
         uc += mine;
       }
@@ -580,7 +562,6 @@ __global__ void __launch_bounds__(xf::kThreads, 1)
       uint32_t g = 0;  // V tiles loaded (ring items 2 g + 1)
       bool ok = true;
       for (Units U(P); U.left > 0 && ok; U.next(P)) {
-        if (!U.loads(P)) continue;
 #pragma unroll 1
         for (int j = U.j0; j < U.j1; ++j, ++g) {
           uint32_t w[KW];
@@ -846,7 +827,6 @@ static cudaError_t launch_fwd(const Problem& p, const MaskTables& m, void* o, fl
   P.tiles = m.tiles;
   P.kv_heads = p.kv_heads;
   P.nsplit = fwd_splits(p);
-  P.resident = P.tiles == 1;
   P.scale_log2 = p.scale * kLog2e;
   const int64_t units = p.bh * P.pairs * P.nsplit;
   if (units > INT32_MAX / 2) return cudaErrorInvalidValue;  // more than the memory holds
@@ -858,9 +838,8 @@ static cudaError_t launch_fwd(const Problem& p, const MaskTables& m, void* o, fl
         align256((size_t)P.nsplit * p.bh * p.np * D * sizeof(float)));
   }
   const int grid = P.units < sm_count() ? P.units : sm_count();
-  const int step = P.resident ? 1 : grid;
-  P.step_pr = step % P.pairs;
-  P.step_bh = step / P.pairs;
+  P.step_pr = grid % P.pairs;
+  P.step_bh = grid / P.pairs;
   k_cross_fwd<D><<<grid, xf::kThreads, S::kBytes, p.s>>>(
       mq, mk, mv, mo, P);
   count_launch();

@@ -321,3 +321,12 @@ def test_no_launch_keeps_a_device_number_per_process():
     for path in bd.sources():
         text = open(path).read()
         assert not re.search(r"static const (int|bool) \w+ = (grid_for|\[\])", text), path
+
+
+def test_a_context_of_one_tile_is_never_the_general_forwards():
+    # k_cross_fwd walks two state tiles or more: up to 64 states every head_dim has the kernel for short
+    # contexts, which needs no workspace, where the general one builds tables of the mask
+    for d in (48, 64, 96, 128):
+        for l in (1, 33, 64):
+            assert b.pack3d_cross_attn_workspace_bytes(1, 1, 2, 2, 300, l, d, True) == 0
+        assert b.pack3d_cross_attn_workspace_bytes(1, 1, 2, 2, 300, 129, d, True) > 0
