@@ -172,3 +172,11 @@ def test_ragged_rows_start_at_any_element(dtype, cols):
         g = p3d().pack3d_layer_norm_bwd(dy[1:], view, w, f)
         for n in ("dx", "dweight", "dbias"):
             assert torch.equal(g[n], wantg[n]), n
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(20001, 128), (10001, 256), (6001, 512), (5001, 1024), (1501, 4096),
+                                       (801, 8192), (301, 16384)])
+def test_rows_of_four_pieces_a_thread_over_many_rows(dtype, rows, cols):
+    # the most registers per thread: several rows for each group of threads, forward and backward
+    run_and_check(*make(rows, cols, dtype, torch.float32, seed=12))
