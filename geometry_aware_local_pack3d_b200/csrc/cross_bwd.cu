@@ -14,9 +14,9 @@
 //   k_cross_sum   the row ranges' partial dk, dv, added in range order (no atomics anywhere).
 // What bounds them: the chain of a step (scores, elementwise pass, second products) through tensor
 // memory, which two CTAs or two warp groups overlap only in part. Measured, 2 x 8 heads of 32,768 rows
-// to 500 padded states of 96: dq 220 us with the tensor pipe 29 % busy and the exponential unit 26 %,
-// dk and dv 193 us with 44 % and 30 %; backward 402 us, 470 TFLOP/s over its five products (seven are
-// formed: S and dP in both kernels).
+// to 500 padded states of 96: dq 224 us with the tensor pipe 28 % busy and the exponential unit 26 %,
+// dk and dv 189 us with 45 % and 30 %; backward 400 to 490 us from box to box, 390 to 480 TFLOP/s over
+// its five products (seven are formed: S and dP in both kernels).
 // A KV head's gradients sum over its query heads, which are rows of the same problem.
 // P and dS are rounded to bf16 for the second products (relative 2^-8, as the outputs).
 // Masked states: in k_cross_dq their dS is zero whatever S and dP hold, and their K rows (which may

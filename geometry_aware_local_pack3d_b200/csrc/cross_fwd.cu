@@ -12,10 +12,12 @@
 // Per state tile: S = q K^T (fp32 in TMEM); the softmax threads read S into registers and hand its
 // columns back at once, so that the next tile's S is formed under this tile's exponentials;
 // P = 2^(s - m) in bf16 goes to columns of its own and O += P V (P read from TMEM).
-// What bounds it: the exponentials (16 a cycle and SM: 1,024 cycles per 256 x 64 scores against 768
-// of tensor work at d = 96, 2^13 FLOP a cycle). Eight softmax warps, two per sub-partition: a warp
-// alone keeps its sub-partition's exponential unit busy half the time (it waits for S, takes maxima,
-// packs, stores). Measured, 2 x 8 heads of 65,536 rows to 1,024 states of 96: 550 us, 750 TFLOP/s.
+// What bounds it: a row tile's chain through tensor memory and barriers (S, maximum, exponentials, P,
+// product), with the exponentials as its longest part (16 a cycle and SM: 1,024 cycles per 256 x 64
+// scores against 768 of tensor work at d = 96, 2^13 FLOP a cycle): their unit is 52 % busy, the tensor
+// pipe 39 %. Eight softmax warps, two per sub-partition: a warp alone keeps its sub-partition's unit
+// busy half the time (it waits for S, takes maxima, packs, stores). Measured, 2 x 8 heads of 65,536
+// rows to 1,024 states of 96: 550 us, 750 TFLOP/s.
 // The running reference m of a row moves only when its maximum has grown by more than 2^8 (p is at
 // most 2^8 and its sum and O are fp32, so nothing overflows and no digits are lost); O is then
 // rescaled in TMEM, which few tiles need after the first.

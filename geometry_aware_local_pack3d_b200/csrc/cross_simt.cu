@@ -2,9 +2,10 @@
 // and backward, head_dim 48, 64, 96 or 128.
 //
 // Tiles of 64 rows x 64 states; 256 threads as 16 x 16, thread (ty, tx) holding rows 4 ty .. + 3
-// and states tx + 16 j of a score tile. What bounds it: the FMA pipe; a thread's 4 x 4 scores take
-// 64 FMAs per 8 shared loads of 16 bytes (measured, 4 x 2,500 rows and states of 128: FMA pipe 46 to
-// 51 %, shared memory 56 to 60 % busy with the 8 warps that an SM holds). The rows of a masked state
+// and states tx + 16 j of a score tile. What bounds it: shared memory and the FMA pipe in turn, with
+// too few warps to fill either; a thread's 4 x 4 scores take 64 FMAs per 8 shared loads of 16 bytes
+// (measured, 4 heads of 2,500 rows to 2,500 states of 128: forward 475 us, backward 1,518; FMA pipe 46
+// to 50 %, shared memory 55 to 59 % busy with the 8 warps that an SM holds). The rows of a masked state
 // are read as zeros, so that nothing they hold reaches a product, and their scores are -inf.
 //   k_cross_fwd32   online softmax over a range of the state tiles, o and lse
 //   k_cross_dq32    dq_i = sum_j dS_ij k_j,            dS = p (dO v - D) tau, over such a range

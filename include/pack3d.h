@@ -293,8 +293,10 @@ size_t pack3d_cross_attn_workspace_bytes(int dtype, int batch, int heads, int kv
  * mask       device bytes [B, L], 0 leaves the state out; NULL: all take part. Nothing that a
  *            state left out holds (infinities, NaN) reaches a result. A row with no state (an
  *            empty mask, L = 0) has o = 0 and lse = -inf.
- * n, l       rows and states, each 0 or more; (H / H_kv) n and l at most 2^30.
+ * n, l       rows and states, each 0 or more; (H / H_kv) n and l at most 2^30, B H at most 65,535
+ *            (UNSUPPORTED beyond).
  * head_dim   48, 64, 96 or 128.
+ * scale      positive and finite.
  * lse        device float32 [B, H, N] or NULL (natural logarithm; what the backward needs).
  * workspace  device, 256-byte aligned, pack3d_cross_attn_workspace_bytes(..., 0) bytes (NULL where
  *            that is 0); contents on entry are ignored. One call at a time may use it.
