@@ -73,7 +73,7 @@ def holds(kernel, numbers, *args):
 
 
 # (row tiles, state tiles) of the units of a CTA: one row tile alone, single state tiles, none
-FORWARD_UNITS = [((2, 3), (1, 2), (2, 1), (2, 1), (1, 4), (2, 2)), ((1, 6), (1, 3), (1, 1))]
+FORWARD_UNITS = [((2, 3), (1, 2), (2, 0), (2, 1), (2, 1), (1, 4), (2, 2)), ((1, 6), (1, 3), (1, 1))]
 
 
 def forward_numbers(numbers, d):

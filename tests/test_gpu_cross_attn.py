@@ -379,3 +379,27 @@ def test_rows_that_are_not_finite_keep_to_their_own_gradients(dtype, mask, N, L,
     none = (~m.any(1))[:, None, None, None].expand_as(q)
     assert bool((g2["dq"][none] == 0).all()) and bool((f2["o"][none] == 0).all())
     assert torch.equal(g2["dq"][~bad], g["dq"][~bad])
+
+
+@pytest.mark.parametrize("d", [48, 64, 96, 128])
+@pytest.mark.parametrize("N,L,mask", [(1000, 700, "none"), (90, 1500, "random"), (3000, 100, "pad")])
+def test_results_under_other_traffic(d, N, L, mask):
+    # another stream copies without a pause, so that this one's copies land late and in other orders
+    m3 = p3d()
+    q, k, v, m, dO = make(2, 4, 2, N, L, d, torch.bfloat16, mask, seed=51, garbage=True)
+    f, g = run_and_check(q, k, v, m, dO)
+    a, b = (torch.empty(1 << 28, dtype=torch.uint8, device="cuda") for _ in range(2))
+    torch.cuda.synchronize()
+    noise, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(10):
+        with torch.cuda.stream(noise):
+            for _ in range(2):
+                b.copy_(a)
+        f2 = m3.pack3d_cross_attn_fwd(q, k, v, mask=m, save_for_backward=True, stream=mine)
+        g2 = m3.pack3d_cross_attn_bwd(q, k, v, f2, dO, mask=m, stream=mine)
+        outs.append((f2, g2))
+    torch.cuda.synchronize()
+    for f2, g2 in outs:
+        assert torch.equal(f["o"], f2["o"]) and torch.equal(f["lse"], f2["lse"])
+        assert all(torch.equal(g[n], g2[n]) for n in ("dq", "dk", "dv"))
